@@ -12,28 +12,39 @@ Low-level (same names and argument order as the C calls):
     nvfp4_quantize_noalloc, nvfp4_layernorm_quantize, nvfp4_quantize_block, nvfp4_block_size_errors, nvfp4_select_block_size,
     nvfp4_dequantize, nvfp4_fake_quantize, nvfp4_ste_backward,
     nvfp4_gemm_w4a4, nvfp4_gemm_w4a4_grouped, nvfp4_gemm_w4a16, nvfp4_mx_sf_bytes, nvfp4_mx_quantize,
-    nvfp4_mx_dequantize, nvfp4_mx_gemm, nvfp4_attention, nvfp4_attention_workspace_bytes, nvfp4_launch_count
+    nvfp4_mx_dequantize, nvfp4_mx_gemm, nvfp4_attention, nvfp4_attention_workspace_bytes, nvfp4_launch_count,
+    nvfp4_gemv_w4a16, nvfp4_rotary, nvfp4_cross_attention, nvfp4_cross_attention_backward,
+    nvfp4_cross_attention_backward_workspace_bytes (include/nvfp4_dit.h)
 Convenience (allocate outputs with torch, then call the above):
     NVFP4Tensor, quantize, layernorm_quantize, dequantize, gemm_w4a4, gemm_w4a4_nvfp4_out, gemm_w4a4_grouped,
     gemm_w4a16,
     fake_quantize, ste_backward, FakeQuantizeSTE (autograd: the two kernels),
     MXTensor, mx_quantize, mx_dequantize, mx_gemm, quantize_block, block_size_errors, select_block_size,
-    attention
+    attention, gemv_w4a16,
+    rotary, RotaryEmbedding (autograd), cross_attention, cross_attention_backward, CrossAttention (autograd)
 """
 from __future__ import annotations
 
 import ctypes
+import math
 from dataclasses import dataclass
 
 import torch
 
-from ._lib import MAX_GROUP, NVFP4Error, NVFP4GemmProblem, check, lib  # noqa: F401
+from ._lib import MAX_GROUP, NVFP4Error, NVFP4GemmProblem, NVFP4Heads, check, lib  # noqa: F401
 
 NVFP4_DTYPE_BF16 = 0
 NVFP4_DTYPE_F32 = 1
 NVFP4_SCALE_GIVEN = 1
 NVFP4_ACT_NONE = 0
 NVFP4_ACT_GELU_TANH = 1
+NVFP4_WEIGHTS_NVFP4 = 0
+NVFP4_WEIGHTS_MX = 1
+NVFP4_GEMV_MAX_ROWS = 16
+NVFP4_POSITION_I32 = 0
+NVFP4_POSITION_F32 = 1
+NVFP4_ROTARY_INTERLEAVED = 1
+NVFP4_ROTARY_INVERSE = 2
 
 _DT = {torch.bfloat16: NVFP4_DTYPE_BF16, torch.float32: NVFP4_DTYPE_F32}
 
@@ -201,6 +212,51 @@ def nvfp4_gemm_w4a16(x, w_codes, w_sf, w_scale, M, N, K, y, y_dtype=NVFP4_DTYPE_
     st = lib().nvfp4_gemm_w4a16(_ptr(x), _ptr(w_codes), _ptr(w_sf), _ptr(w_scale), M, N, K, _ptr(y),
                                 y_dtype, _ptr(dev_status), _stream(stream))
     check(st, "nvfp4_gemm_w4a16")
+
+
+def _heads(t) -> NVFP4Heads | None:
+    """A [batch, tokens, heads, d] tensor (d contiguous) as nvfp4_heads."""
+    if t is None:
+        return None
+    if not t.is_cuda:
+        raise ValueError("tensor must live on a CUDA device")
+    sb, sl, sh, _ = t.stride()
+    return NVFP4Heads(t.data_ptr(), sb, sl, sh)
+
+
+def nvfp4_gemv_w4a16(x, ld_x, w_codes, w_sf, w_scale, w_format, bias, M, N, K, y, y_dtype=NVFP4_DTYPE_BF16,
+                     stream=None) -> None:
+    check(lib().nvfp4_gemv_w4a16(_ptr(x), ld_x, _ptr(w_codes), _ptr(w_sf), _ptr(w_scale), w_format, _ptr(bias), M, N,
+                                 K, _ptr(y), y_dtype, _stream(stream)), "nvfp4_gemv_w4a16")
+
+
+def nvfp4_rotary(x, positions, pos_dtype, pos_batch_stride, pos_token_stride, axis_dims, theta, B, L, H, d, dtype,
+                 flags, out, stream=None) -> None:
+    """``x`` and ``out``: [B, L, H, d] tensors; ``axis_dims``: a sequence of ints."""
+    dims = (ctypes.c_int * len(axis_dims))(*axis_dims)
+    check(lib().nvfp4_rotary(ctypes.byref(_heads(x)), _ptr(positions), pos_dtype, pos_batch_stride, pos_token_stride,
+                             dims, len(axis_dims), theta, B, L, H, d, dtype, flags, ctypes.byref(_heads(out)),
+                             _stream(stream)), "nvfp4_rotary")
+
+
+def nvfp4_cross_attention(q, k, v, kv_lens, scale, B, H, Hkv, Lq, Lk, d, out, lse, dev_status=None,
+                          stream=None) -> None:
+    """``q``, ``k``, ``v``, ``out``: [batch, tokens, heads, d] tensors."""
+    check(lib().nvfp4_cross_attention(*(ctypes.byref(_heads(t)) for t in (q, k, v)), _ptr(kv_lens), scale, B, H, Hkv,
+                                      Lq, Lk, d, ctypes.byref(_heads(out)), _ptr(lse), _ptr(dev_status),
+                                      _stream(stream)), "nvfp4_cross_attention")
+
+
+def nvfp4_cross_attention_backward_workspace_bytes(B: int, H: int, Hkv: int, Lq: int, Lk: int, d: int) -> int:
+    return int(lib().nvfp4_cross_attention_backward_workspace_bytes(B, H, Hkv, Lq, Lk, d))
+
+
+def nvfp4_cross_attention_backward(grad_out, q, k, v, out, lse, kv_lens, scale, B, H, Hkv, Lq, Lk, d, dq, dk, dv,
+                                   workspace, workspace_bytes, dev_status=None, stream=None) -> None:
+    check(lib().nvfp4_cross_attention_backward(
+        *(ctypes.byref(_heads(t)) for t in (grad_out, q, k, v, out)), _ptr(lse), _ptr(kv_lens), scale, B, H, Hkv, Lq,
+        Lk, d, *(ctypes.byref(_heads(t)) for t in (dq, dk, dv)), _ptr(workspace), workspace_bytes, _ptr(dev_status),
+        _stream(stream)), "nvfp4_cross_attention_backward")
 
 
 # ----------------------------------------------------------------- convenience
@@ -470,3 +526,180 @@ def attention(q: NVFP4Tensor, k: NVFP4Tensor, v: NVFP4Tensor, H: int, s_head: to
     nvfp4_attention(q.codes, q.sf, q.scale, k.codes, k.sf, k.scale, v.codes, v.sf, v.scale, s_head, H, Lq, Lk, d, o,
                     workspace, wsb, dev_status, stream)
     return o
+
+
+# ----------------------------------------------------------------- around the linear layers
+def _require(ok: bool, what: str) -> None:
+    if not ok:
+        raise ValueError(what)
+
+
+def _on_device(*tensors) -> None:
+    """Every given tensor lives on the current CUDA device, where the kernels run."""
+    here = torch.cuda.current_device() if torch.cuda.is_available() else None
+    for t in tensors:
+        if t is not None:
+            _require(t.is_cuda and t.device.index == here, f"tensor on {t.device}: the call runs on the current CUDA device")
+
+
+def _used_on(stream, *tensors) -> None:
+    """Tensors a call allocated (on the current stream) stay unrecycled until
+    the other stream the call runs on has passed."""
+    if stream is None:
+        return
+    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
+    if s != torch.cuda.current_stream():
+        for t in tensors:
+            t.record_stream(s)
+
+
+def gemv_w4a16(x: torch.Tensor, w: NVFP4Tensor | MXTensor, bias: torch.Tensor | None = None,
+               out_dtype=torch.bfloat16, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Y = X W^T (+ bias) for at most NVFP4_GEMV_MAX_ROWS rows: X bf16 [M, K]
+    (rows may be strided), W NVFP4 or MX [N, K], bias FP32 [N], Y bf16 or FP32."""
+    mx = isinstance(w, MXTensor)
+    _require(x.dtype == torch.bfloat16 and x.dim() == 2 and x.shape[1] == w.k, "x must be bf16 [M, w.k]")
+    _require(x.shape[0] <= NVFP4_GEMV_MAX_ROWS, f"at most {NVFP4_GEMV_MAX_ROWS} rows: gemm_w4a16 takes more")
+    _require(x.stride(1) == 1, "x must be contiguous along k")
+    _require(bias is None or (bias.dtype == torch.float32 and bias.shape == (w.rows,) and bias.is_contiguous()),
+             "bias must be a contiguous FP32 [N]")
+    M = x.shape[0]
+    y = out if out is not None else torch.empty(M, w.rows, dtype=out_dtype, device=x.device)
+    _require(y.dtype in _DT and y.shape == (M, w.rows) and y.is_contiguous(), "out must be a contiguous bf16 or FP32 [M, N]")
+    _on_device(x, w.codes, w.sf, None if mx else w.scale, bias, y)
+    nvfp4_gemv_w4a16(x, max(x.stride(0), w.k), w.codes, w.sf, None if mx else w.scale,
+                     NVFP4_WEIGHTS_MX if mx else NVFP4_WEIGHTS_NVFP4, bias, M, w.rows, w.k, y, _DT[y.dtype], stream)
+    if out is None:
+        _used_on(stream, y)
+    return y
+
+
+def _rows16(t: torch.Tensor) -> torch.Tensor:
+    """t with its last axis contiguous and 16-byte steps (a copy where it has not)."""
+    n = 16 // t.element_size()
+    if t.stride(-1) == 1 and t.data_ptr() % 16 == 0 and all(
+            s % n == 0 and (s >= t.shape[-1] or (s == 0 and i != 1)) for i, (s, size) in
+            enumerate(zip(t.stride()[:-1], t.shape)) if size > 1):
+        return t
+    return t.contiguous()
+
+
+def rotary(x: torch.Tensor, positions: torch.Tensor, axes, theta: float = 10000.0, interleaved: bool = True,
+           inverse: bool = False, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Rotary positions with several axes: x [B, L, H, d] (bf16 or FP32, strided
+    views such as a part of a fused projection included), positions int32 or
+    FP32 [L, n_axes] or [B, L, n_axes], ``axes`` the values of a head each axis
+    turns (even, together at most d; the rest is copied).  Pairs are neighbours
+    (``interleaved``) or halves of the turned part; ``inverse`` turns back.
+    ``out``: any [B, L, H, d] view (for instance of a [B, H, L, d] buffer, whose
+    rows quantize() takes), or x itself."""
+    _require(x.dim() == 4 and x.dtype in _DT and x.stride(3) == 1, "x must be bf16 or FP32 [B, L, H, d], d contiguous")
+    B, L, H, d = x.shape
+    axes = tuple(int(a) for a in axes)
+    _require(positions.dtype in (torch.int32, torch.float32) and positions.dim() in (2, 3)
+             and tuple(positions.shape[-2:]) == (L, len(axes)) and (positions.dim() == 2 or positions.shape[0] in (1, B)),
+             "positions must be int32 or FP32 [L, n_axes] or [B, L, n_axes]")
+    _require(positions.stride(-1) == 1 or len(axes) == 1, "positions must be contiguous along the axes")
+    y = out if out is not None else torch.empty(B, L, H, d, dtype=x.dtype, device=x.device)
+    _require(y.dtype == x.dtype and y.shape == x.shape and y.stride(3) == 1, "out must match x, d contiguous")
+    _on_device(x, positions, y)
+    flags = (NVFP4_ROTARY_INTERLEAVED if interleaved else 0) | (NVFP4_ROTARY_INVERSE if inverse else 0)
+    per_sample = positions.dim() == 3 and positions.shape[0] > 1
+    nvfp4_rotary(x, positions, NVFP4_POSITION_I32 if positions.dtype == torch.int32 else NVFP4_POSITION_F32,
+                 positions.stride(0) if per_sample else 0, positions.stride(-2), axes, float(theta), B, L, H, d,
+                 _DT[x.dtype], flags, y, stream)
+    if out is None:
+        _used_on(stream, y)
+    return y
+
+
+class RotaryEmbedding(torch.autograd.Function):
+    """Autograd wrapper of rotary(): the backward pass turns the gradient back.
+    Positions get no gradient.  As for any torch operator, a backward pass is
+    captured into a CUDA graph from leaves of the capture's own (x.detach()
+    .requires_grad_()): an eager graph of the same leaves invalidates it."""
+
+    @staticmethod
+    def forward(ctx, x, positions, axes, theta=10000.0, interleaved=True):
+        ctx.save_for_backward(positions)
+        ctx.how = (axes, theta, interleaved)
+        return rotary(x, positions, axes, theta, interleaved)
+
+    @staticmethod
+    def backward(ctx, grad):
+        (positions,) = ctx.saved_tensors
+        return rotary(_rows16(grad), positions, *ctx.how, inverse=True), None, None, None, None
+
+
+def _attention_sizes(q, k, v, kv_lens):
+    for t in (q, k, v):
+        _require(t.dim() == 4 and t.dtype == torch.bfloat16 and t.stride(3) == 1,
+                 "q, k and v must be bf16 [batch, tokens, heads, d], d contiguous")
+    B, Lq, H, d = q.shape
+    Lk, Hkv = k.shape[1], k.shape[2]
+    _require(k.shape == (B, Lk, Hkv, d) and v.shape == k.shape, "k and v must be [B, Lk, Hkv, d] of q's B and d")
+    _require(kv_lens is None or (kv_lens.dtype == torch.int32 and kv_lens.shape == (B,) and kv_lens.is_contiguous()),
+             "kv_lens must be a contiguous int32 [B]")
+    return B, H, Hkv, Lq, Lk, d
+
+
+def cross_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, kv_lens: torch.Tensor | None = None,
+                    scale: float | None = None, out: torch.Tensor | None = None, return_lse: bool = False,
+                    dev_status=None, stream=None):
+    """softmax(scale q k^T) v: q [B, Lq, H, d], k and v [B, Lk, Hkv, d] (bf16,
+    strided views included, d % 8 == 0 up to 128, Hkv divides H), over the first
+    kv_lens[b] keys of sample b (all of them without kv_lens).  scale defaults
+    to 1 / sqrt(d).  Returns bf16 [B, Lq, H, d], and with ``return_lse`` the FP32
+    [B, H, Lq] log-sum-exp that cross_attention_backward() takes."""
+    B, H, Hkv, Lq, Lk, d = sizes = _attention_sizes(q, k, v, kv_lens)
+    o = out if out is not None else torch.empty(B, Lq, H, d, dtype=torch.bfloat16, device=q.device)
+    _require(o.dtype == torch.bfloat16 and o.shape == q.shape and o.stride(3) == 1, "out must be a bf16 tensor of q's shape")
+    lse = torch.empty(B, H, Lq, dtype=torch.float32, device=q.device) if return_lse else None
+    _on_device(q, k, v, kv_lens, o, dev_status)
+    nvfp4_cross_attention(q, k, v, kv_lens, 1.0 / math.sqrt(d) if scale is None else float(scale), *sizes, o, lse,
+                          dev_status, stream)
+    if stream is not None:
+        _used_on(stream, *(t for t in (o if out is None else None, lse) if t is not None))
+    return (o, lse) if return_lse else o
+
+
+def cross_attention_backward(grad_out: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                             out: torch.Tensor, lse: torch.Tensor, kv_lens: torch.Tensor | None = None,
+                             scale: float | None = None, workspace: torch.Tensor | None = None, dev_status=None,
+                             stream=None):
+    """(dq, dk, dv) of cross_attention() from its ``out`` and ``lse``."""
+    B, H, Hkv, Lq, Lk, d = sizes = _attention_sizes(q, k, v, kv_lens)
+    for t in (grad_out, out):
+        _require(t.dtype == torch.bfloat16 and t.shape == q.shape and t.stride(3) == 1,
+                 "grad_out and out must be bf16 tensors of q's shape, d contiguous")
+    _require(lse.dtype == torch.float32 and lse.shape == (B, H, Lq) and lse.is_contiguous(),
+             "lse must be a contiguous FP32 [B, H, Lq]")
+    need = nvfp4_cross_attention_backward_workspace_bytes(*sizes)
+    ws = workspace if workspace is not None else torch.empty(need, dtype=torch.uint8, device=q.device)
+    _require(ws.is_contiguous(), "workspace must be contiguous")
+    dq = torch.empty(B, Lq, H, d, dtype=torch.bfloat16, device=q.device)
+    dk, dv = (torch.empty(B, Lk, Hkv, d, dtype=torch.bfloat16, device=q.device) for _ in range(2))
+    _on_device(grad_out, q, k, v, out, lse, kv_lens, ws, dev_status)
+    nvfp4_cross_attention_backward(grad_out, q, k, v, out, lse, kv_lens, 1.0 / math.sqrt(d) if scale is None else
+                                   float(scale), *sizes, dq, dk, dv, ws, ws.numel() * ws.element_size(), dev_status,
+                                   stream)
+    if stream is not None:
+        _used_on(stream, dq, dk, dv, *((ws,) if workspace is None else ()))
+    return dq, dk, dv
+
+
+class CrossAttention(torch.autograd.Function):
+    """Autograd wrapper of cross_attention() and cross_attention_backward():
+    gradients of q, k and v.  Captured into a CUDA graph as RotaryEmbedding is."""
+
+    @staticmethod
+    def forward(ctx, q, k, v, kv_lens=None, scale=None):
+        out, lse = cross_attention(q, k, v, kv_lens, scale, return_lse=True)
+        ctx.save_for_backward(q, k, v, out, lse, kv_lens)
+        ctx.scale = scale
+        return out
+
+    @staticmethod
+    def backward(ctx, grad):
+        q, k, v, out, lse, kv_lens = ctx.saved_tensors
+        return (*cross_attention_backward(_rows16(grad), q, k, v, out, lse, kv_lens, ctx.scale), None, None)

@@ -36,7 +36,13 @@ class NVFP4GemmProblem(ctypes.Structure):
 
 MAX_GROUP = 8
 
-# every symbol include/nvfp4.h declares, with (restype, argtypes)
+
+class NVFP4Heads(ctypes.Structure):
+    """nvfp4_heads (include/nvfp4_dit.h): a [batch, tokens, heads, d] operand."""
+    _fields_ = [("data", _p), ("batch_stride", _i64), ("token_stride", _i64), ("head_stride", _i64)]
+
+
+# every symbol include/nvfp4.h and include/nvfp4_dit.h declare, with (restype, argtypes)
 SIGNATURES = {
     "nvfp4_sf_bytes": (ctypes.c_size_t, [_i64, _i64]),
     "nvfp4_quantize_workspace_bytes": (ctypes.c_size_t, [_i64, _i64]),
@@ -67,6 +73,14 @@ SIGNATURES = {
     "nvfp4_launch_count": (ctypes.c_uint64, []),
     "nvfp4_shutdown": (None, []),
     "nvfp4_debug_wait_timeout": (_status, [_p, _i64, _p]),
+    "nvfp4_gemv_w4a16": (_status, [_p, _i64, _p, _p, _p, _int, _p, _i64, _i64, _i64, _p, _int, _p]),
+    "nvfp4_rotary": (_status, [_p, _p, _int, _i64, _i64, _p, _int, ctypes.c_double, _i64, _i64, _i64, _i64, _int,
+                               ctypes.c_uint, _p, _p]),
+    "nvfp4_cross_attention": (_status, [_p, _p, _p, _p, ctypes.c_float, _i64, _i64, _i64, _i64, _i64, _i64, _p, _p,
+                                        _p, _p]),
+    "nvfp4_cross_attention_backward_workspace_bytes": (ctypes.c_size_t, [_i64] * 6),
+    "nvfp4_cross_attention_backward": (_status, [_p, _p, _p, _p, _p, _p, _p, ctypes.c_float, _i64, _i64, _i64, _i64,
+                                                 _i64, _i64, _p, _p, _p, _p, ctypes.c_size_t, _p, _p]),
 }
 
 

@@ -7,9 +7,9 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libnvfp4.so")
 SOURCES = ["api.cu", "quantize.cu", "quantize_noalloc.cu", "layernorm.cu", "mx.cu", "blocksize.cu", "attn.cu", "gemm_w4a4.cu",
-           "gemm_w4a4_2sm.cu", "gemm_w4a16.cu"]
-HEADERS = ["ptx.cuh", "quant_math.cuh", "epilogue.cuh", "internal.h", "gemm.h", "tmap.h"]
-INCLUDE = os.path.join(os.path.dirname(HERE), "include", "nvfp4.h")
+           "gemm_w4a4_2sm.cu", "gemm_w4a16.cu", "api_dit.cu", "gemv.cu", "rotary.cu", "xattn.cu"]
+HEADERS = ["ptx.cuh", "quant_math.cuh", "epilogue.cuh", "internal.h", "gemm.h", "tmap.h", "dit.h"]
+INCLUDES = [os.path.join(os.path.dirname(HERE), "include", f) for f in ("nvfp4.h", "nvfp4_dit.h")]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -24,7 +24,7 @@ def _stale() -> bool:
     if not os.path.exists(LIB):
         return True
     t = os.path.getmtime(LIB)
-    deps = [os.path.join(CSRC, f) for f in SOURCES + HEADERS] + [INCLUDE, __file__]
+    deps = [os.path.join(CSRC, f) for f in SOURCES + HEADERS] + INCLUDES + [__file__]
     return any(os.path.getmtime(d) > t for d in deps)
 
 

@@ -58,7 +58,7 @@ struct DevInfo {
 };
 static DevInfo g_dev[64];
 
-static nvfp4_status device_ok(int* sms) {
+nvfp4_status device_ok(int* sms) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return NVFP4_ERR_CUDA;
     if (dev < 0 || dev >= 64) return NVFP4_ERR_UNSUPPORTED_DEVICE;

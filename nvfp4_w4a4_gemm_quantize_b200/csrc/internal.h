@@ -4,7 +4,13 @@
 #include <cstdint>
 #include <cuda_runtime.h>
 
+#include "../../include/nvfp4.h"
+
 namespace nvfp4 {
+
+// The current device is one the library runs on (cached per device); its
+// number of SMs in *sms when given.
+nvfp4_status device_ok(int* sms);
 
 constexpr int kAmaxThreads = 512;
 constexpr int kAmaxMaxCtas = 256;        // partial maxima, one float each

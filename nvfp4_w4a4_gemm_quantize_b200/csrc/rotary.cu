@@ -1,0 +1,234 @@
+// rotary.cu -- rotary positions with several axes (nvfp4_rotary).
+//
+// Pair j of a token's head turns by angle[token, j] = position[axis(j)] *
+// theta^(-2 i / width(axis)); the angles do not depend on the head, so a block
+// takes a few tokens, forms their cos / sin once in shared memory and turns
+// every head with them.  The angle is formed in turns (the frequencies come
+// divided by 2 pi, in FP64 from the host) and reduced to half a turn in FP64:
+// three FP64 operations per token and pair, against 2 H elements moved.
+// Bound by memory: every element is read and written once.
+#include <cmath>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "dit.h"
+#include "internal.h"
+
+namespace nvfp4 {
+namespace rotary {
+
+constexpr int kThreads = 256;
+constexpr int kAhead = 4;                 // vectors a thread loads before it waits for the angles
+constexpr int kMaxTokens = 32;            // tokens of a block
+
+// n / d for 0 <= n < 2^31 as a multiplication (d >= 1): m = ceil(2^(31 + s) / d), 2^s >= d.
+struct FastDiv {
+    uint32_t d, m, s;                     // H d <= 2^26 (checked by the entry point), so 32 tokens stay below 2^31
+};
+
+FastDiv fast_div(uint32_t d) {
+    FastDiv f{d, 0, 0};
+    while ((1ull << f.s) < d) ++f.s;
+    f.m = (uint32_t)(((1ull << (31 + f.s)) + d - 1) / d);
+    return f;
+}
+
+__device__ __forceinline__ uint32_t divide(uint32_t n, const FastDiv& f) {
+    return (uint32_t)(((uint64_t)n * f.m) >> (31 + f.s));
+}
+
+struct Params {
+    nvfp4_heads x, out;
+    const void* positions;
+    int64_t pos_batch_stride, pos_token_stride;
+    bool pos_f32;
+    int L, H, pairs;
+    int tokens, tiles;                    // tokens of a block, blocks of a sample
+    FastDiv units, heads_units;           // vectors of a head, of a token
+    int rotated_units;                    // vectors of a head that hold pairs (split pairs: of each half)
+    float sign;                           // -1: turn back
+    double turns[kRotaryMaxPairs];        // frequency of a pair, turns per position
+    uint8_t axis[kRotaryMaxPairs];
+};
+
+template <int BYTES>
+struct Word;
+template <>
+struct Word<16> { typedef uint4 type; };
+template <>
+struct Word<8> { typedef uint2 type; };
+template <>
+struct Word<4> { typedef uint32_t type; };
+template <>
+struct Word<2> { typedef uint16_t type; };
+
+// W values of type T (bf16 as its 16 bits, or FP32) moved as one word.
+template <typename T, int W>
+union Vec {
+    typename Word<sizeof(T) * W>::type word;
+    T v[W];
+};
+
+__device__ __forceinline__ float to_f32(uint16_t b) { return __uint_as_float((uint32_t)b << 16); }
+__device__ __forceinline__ float to_f32(float f) { return f; }
+__device__ __forceinline__ void from_f32(float f, uint16_t& b) { b = __bfloat16_as_ushort(__float2bfloat16_rn(f)); }
+__device__ __forceinline__ void from_f32(float f, float& o) { o = f; }
+
+// (u, v) turned; the two products of a sum are rounded as the compiler contracts them.
+__device__ __forceinline__ void turn(float& u, float& v, float2 cs) {
+    const float a = u * cs.x - v * cs.y, b = u * cs.y + v * cs.x;
+    u = a;
+    v = b;
+}
+
+template <typename T, int W, bool INTERLEAVED>
+__global__ void __launch_bounds__(kThreads)
+rotary_kernel(const __grid_constant__ Params p) {
+    extern __shared__ float2 cs[];        // [tokens][pairs]
+    const int b = blockIdx.x / p.tiles;
+    const int l0 = (int)(blockIdx.x - b * p.tiles) * p.tokens;
+    const int tokens = min(p.tokens, p.L - l0);
+    const uint32_t total = (uint32_t)tokens * p.heads_units.d;
+    const T* x = static_cast<const T*>(p.x.data) + (int64_t)b * p.x.batch_stride;
+    T* out = static_cast<T*>(p.out.data) + (int64_t)b * p.out.batch_stride;
+
+    Vec<T, W> lo[kAhead], hi[kAhead];
+    // vector u of the block: token, head and place in the head; with split
+    // pairs a place holds a vector of each half, or a copied one
+    auto place = [&](uint32_t u, int& token, int& head, int& unit) {
+        token = (int)divide(u, p.heads_units);
+        const uint32_t r = u - (uint32_t)token * p.heads_units.d;
+        head = (int)divide(r, p.units);
+        unit = (int)(r - (uint32_t)head * p.units.d);
+    };
+    auto column = [&](int unit) {         // first column of a vector
+        return INTERLEAVED || unit < p.rotated_units ? unit * W : p.pairs + unit * W;
+    };
+    auto load = [&](uint32_t first) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            const uint32_t u = first + i * kThreads;
+            if (u >= total) break;
+            int token, head, unit;
+            place(u, token, head, unit);
+            const T* src = x + (int64_t)(l0 + token) * p.x.token_stride + (int64_t)head * p.x.head_stride + column(unit);
+            lo[i].word = *reinterpret_cast<const decltype(lo[i].word)*>(src);
+            if (!INTERLEAVED && unit < p.rotated_units)
+                hi[i].word = *reinterpret_cast<const decltype(hi[i].word)*>(src + p.pairs);
+        }
+    };
+
+    load(threadIdx.x);
+    for (int i = threadIdx.x; i < tokens * p.pairs; i += kThreads) {
+        const int token = i / p.pairs, j = i - token * p.pairs;
+        const int64_t at = (int64_t)b * p.pos_batch_stride + (int64_t)(l0 + token) * p.pos_token_stride + p.axis[j];
+        const double position = p.pos_f32 ? (double)static_cast<const float*>(p.positions)[at]
+                                          : (double)static_cast<const int32_t*>(p.positions)[at];
+        const double t = position * p.turns[j];
+        float s, c;
+        sincospif((float)(2.0 * (t - rint(t))), &s, &c);
+        cs[i] = make_float2(c, p.sign * s);
+    }
+    __syncthreads();
+
+    for (uint32_t first = threadIdx.x; first < total; first += kAhead * kThreads) {
+        if (first != threadIdx.x) load(first);
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            const uint32_t u = first + i * kThreads;
+            if (u >= total) break;
+            int token, head, unit;
+            place(u, token, head, unit);
+            T* dst = out + (int64_t)(l0 + token) * p.out.token_stride + (int64_t)head * p.out.head_stride + column(unit);
+            const float2* a = cs + token * p.pairs;
+            if (INTERLEAVED) {
+#pragma unroll
+                for (int e = 0; e < W; e += 2) {
+                    const int j = (unit * W + e) >> 1;
+                    if (j < p.pairs) {
+                        float f = to_f32(lo[i].v[e]), g = to_f32(lo[i].v[e + 1]);
+                        turn(f, g, a[j]);
+                        from_f32(f, lo[i].v[e]);
+                        from_f32(g, lo[i].v[e + 1]);
+                    }
+                }
+            } else if (unit < p.rotated_units) {
+#pragma unroll
+                for (int e = 0; e < W; ++e) {
+                    float f = to_f32(lo[i].v[e]), g = to_f32(hi[i].v[e]);
+                    turn(f, g, a[unit * W + e]);
+                    from_f32(f, lo[i].v[e]);
+                    from_f32(g, hi[i].v[e]);
+                }
+                *reinterpret_cast<decltype(hi[i].word)*>(dst + p.pairs) = hi[i].word;
+            }
+            *reinterpret_cast<decltype(lo[i].word)*>(dst) = lo[i].word;
+        }
+    }
+}
+
+template <typename T, int W, bool INTERLEAVED>
+cudaError_t launch(const Params& p, int64_t blocks, cudaStream_t stream) {
+    rotary_kernel<T, W, INTERLEAVED><<<(unsigned)blocks, kThreads, (size_t)p.tokens * p.pairs * sizeof(float2), stream>>>(p);
+    const cudaError_t e = cudaGetLastError();
+    if (e == cudaSuccess) count_launch(1);
+    return e;
+}
+
+// The widest vector (at most 16 bytes) that divides `a` and `b` values.
+int vector_values(int64_t a, int64_t b, int most) {
+    int w = most;
+    while (w > 1 && (a % w != 0 || b % w != 0)) w /= 2;
+    return w;
+}
+
+}  // namespace rotary
+
+cudaError_t launch_rotary(const RotaryArgs& a, int num_sms, cudaStream_t stream) {
+    using namespace rotary;
+    Params p{};
+    p.x = a.x;
+    p.out = a.out;
+    p.positions = a.positions;
+    p.pos_batch_stride = a.pos_batch_stride;
+    p.pos_token_stride = a.pos_token_stride;
+    p.pos_f32 = a.pos_f32;
+    p.L = (int)a.L;
+    p.H = (int)a.H;
+    p.pairs = a.pairs;
+    p.sign = a.inverse ? -1.0f : 1.0f;
+    int j = 0;
+    for (int i = 0; i < a.n_axes; ++i)
+        for (int k = 0; k < a.axis_pairs[i]; ++k, ++j) {
+            p.turns[j] = std::pow(a.theta, -(double)k / a.axis_pairs[i]) / 6.283185307179586476925287;
+            p.axis[j] = (uint8_t)i;
+        }
+    const int most = a.f32 ? 4 : 8;
+    // interleaved pairs: d % 8 == 0, so full vectors; split pairs: a vector
+    // must not straddle the halves or the copied tail
+    const int w = a.interleaved ? most : vector_values(a.pairs, a.d - 2 * a.pairs, most);
+    const int units = a.interleaved ? (int)a.d / w : (a.pairs + (int)(a.d - 2 * a.pairs)) / w;
+    p.rotated_units = a.interleaved ? units : a.pairs / w;
+    p.units = fast_div((uint32_t)units);
+    p.heads_units = fast_div((uint32_t)(a.H * units));
+    // tokens of a block: 8 vectors a thread, fewer while the blocks would not fill the SMs twice
+    int64_t tokens = (8 * kThreads + a.H * units - 1) / (a.H * units);
+    if (tokens > kMaxTokens) tokens = kMaxTokens;
+    while (tokens > 1 && a.B * ((a.L + tokens - 1) / tokens) < 2 * num_sms) tokens = (tokens + 1) / 2;
+    p.tokens = (int)tokens;
+    p.tiles = (int)((a.L + tokens - 1) / tokens);
+    const int64_t blocks = a.B * p.tiles;
+    if (a.f32) {
+        if (a.interleaved) return launch<float, 4, true>(p, blocks, stream);
+        if (w == 4) return launch<float, 4, false>(p, blocks, stream);
+        if (w == 2) return launch<float, 2, false>(p, blocks, stream);
+        return launch<float, 1, false>(p, blocks, stream);
+    }
+    if (a.interleaved) return launch<uint16_t, 8, true>(p, blocks, stream);
+    if (w == 8) return launch<uint16_t, 8, false>(p, blocks, stream);
+    if (w == 4) return launch<uint16_t, 4, false>(p, blocks, stream);
+    if (w == 2) return launch<uint16_t, 2, false>(p, blocks, stream);
+    return launch<uint16_t, 1, false>(p, blocks, stream);
+}
+
+}  // namespace nvfp4
