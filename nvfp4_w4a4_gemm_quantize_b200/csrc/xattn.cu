@@ -7,7 +7,7 @@
 #include "internal.h"
 
 namespace nvfp4 {
-namespace xattn {
+namespace xattn_rows {
 
 constexpr int kThreads = 128;
 constexpr int kPer = 4;                   // values of a head a lane holds (columns lane + 32 i)
@@ -35,29 +35,6 @@ __device__ __forceinline__ float dot(const float (&a)[kPer], const float (&b)[kP
 }
 __device__ __forceinline__ int keys_of(const CrossAttnArgs& a, int b) {
     return a.kv_lens ? min(max(a.kv_lens[b], 0), a.Lk) : a.Lk;
-}
-
-__global__ void __launch_bounds__(kThreads) forward_kernel(const CrossAttnArgs a) {
-    const int64_t row = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31;
-    if (row >= (int64_t)a.B * a.H * a.Lq) return;
-    const int l = (int)(row % a.Lq), h = (int)(row / a.Lq % a.H), b = (int)(row / a.Lq / a.H), hk = h / (a.H / a.Hkv);
-    const int n = keys_of(a, b);
-    float q[kPer], k[kPer], v[kPer], o[kPer] = {}, m = -INFINITY, sum = 0.0f;
-    load_row(a.q, b, l, h, a.d, lane, q);
-    for (int j = 0; j < n; ++j) {
-        load_row(a.k, b, j, hk, a.d, lane, k);
-        load_row(a.v, b, j, hk, a.d, lane, v);
-        const float s = a.scale * dot(q, k), m2 = fmaxf(m, s), w = __expf(m - m2), p = __expf(s - m2);
-        sum = sum * w + p;
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) o[i] = o[i] * w + p * v[i];
-        m = m2;
-    }
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) o[i] = n > 0 ? o[i] / sum : 0.0f;
-    store_row(a.out, b, l, h, a.d, lane, o);
-    if (lane == 0 && a.lse) a.lse[row] = n > 0 ? m + logf(sum) : -INFINITY;
 }
 
 __global__ void __launch_bounds__(kThreads) dq_kernel(const CrossAttnArgs a, float* delta) {
@@ -110,14 +87,7 @@ __global__ void __launch_bounds__(kThreads) dkv_kernel(const CrossAttnArgs a, co
 
 unsigned blocks_of(int64_t rows) { return (unsigned)((rows + kThreads / 32 - 1) / (kThreads / 32)); }
 
-}  // namespace xattn
-
-cudaError_t launch_cross_attention(const CrossAttnArgs& a, int, cudaStream_t stream) {
-    xattn::forward_kernel<<<xattn::blocks_of((int64_t)a.B * a.H * a.Lq), xattn::kThreads, 0, stream>>>(a);
-    const cudaError_t e = cudaGetLastError();
-    if (e == cudaSuccess) count_launch(1);
-    return e;
-}
+}  // namespace xattn_rows
 
 size_t cross_attention_backward_workspace(int64_t B, int64_t H, int64_t, int64_t Lq, int64_t, int64_t) {
     return (size_t)(B * H * Lq) * sizeof(float);
@@ -126,8 +96,8 @@ size_t cross_attention_backward_workspace(int64_t B, int64_t H, int64_t, int64_t
 cudaError_t launch_cross_attention_backward(const CrossAttnArgs& a, int, cudaStream_t stream) {
     float* delta = static_cast<float*>(a.workspace);
     const int64_t rows = (int64_t)a.B * a.H * a.Lq, keys = (int64_t)a.B * a.Hkv * a.Lk;
-    if (rows > 0) xattn::dq_kernel<<<xattn::blocks_of(rows), xattn::kThreads, 0, stream>>>(a, delta);
-    if (keys > 0) xattn::dkv_kernel<<<xattn::blocks_of(keys), xattn::kThreads, 0, stream>>>(a, delta);
+    if (rows > 0) xattn_rows::dq_kernel<<<xattn_rows::blocks_of(rows), xattn_rows::kThreads, 0, stream>>>(a, delta);
+    if (keys > 0) xattn_rows::dkv_kernel<<<xattn_rows::blocks_of(keys), xattn_rows::kThreads, 0, stream>>>(a, delta);
     const cudaError_t e = cudaGetLastError();
     if (e == cudaSuccess) count_launch((rows > 0) + (keys > 0));
     return e;

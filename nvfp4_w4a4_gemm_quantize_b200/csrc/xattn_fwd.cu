@@ -1,0 +1,454 @@
+// xattn_fwd.cu -- attention to an encoder's states of another length, forward
+// (nvfp4_cross_attention), for more than a few queries.
+//
+//   S = Q K^T, P = 2^(c S - m) with c = scale log2(e), O = P V / sum P
+// with an online softmax: m is a running reference maximum, sum P and O are
+// rescaled when it moves.  m moves only when a tile exceeds it by more than 8
+// (P stays below 2^8; nothing is lost in FP32), so most tiles touch O only
+// through the tensor cores.
+//
+// Persistent, one CTA per SM.  A work item is a pair of 128-query tiles A and B
+// that read the same keys: consecutive tiles of the query heads of one sample's
+// key / value head (so heads that share one pair up too; a last odd tile runs
+// alone).  Keys come in tiles of 128; the last one computes only as many as it
+// holds, rounded up to 16.
+// TMEM (512 columns): S_A, S_B, O_A, O_B.  P overwrites its S as packed bf16
+// and is the A operand of the second product from there.  One warp issues every
+// product, in the order S_A S_B | P V_A, next S_A | P V_B, next S_B | ...: the
+// tensor core works for one tile while the other's softmax runs, and S of the
+// next tile needs no barrier of its own, since the tensor core takes it after
+// the product that read P.  The order runs on across work items.
+// Warps: 0 loads (three rotating Q tiles, a ring of K and V tiles), 1 issues
+// and owns TMEM, 4-7 and 8-11 softmax and output of A and B, a thread per row.
+// Bound by the exponentials and the tensor core about equally at d = 128 (a
+// pair of 128 x 128 tiles costs 2048 cycles of either), by the exponentials below.
+#include "xattn.cuh"
+
+namespace nvfp4 {
+namespace xattn {
+
+constexpr int kThreads = 384;
+constexpr int kQBufs = 3;
+constexpr int kMaxRing = 12;
+constexpr int kRegsLow = 64;                  // 128 x 64 + 256 x 208 <= 384 x 168
+constexpr int kRegsHigh = 208;
+static_assert(128 * kRegsLow + 256 * kRegsHigh <= kThreads * 168, "register split exceeds the launch budget");
+
+constexpr uint32_t kColS = 0;                 // S_g (and P_g): [128 g, 128 g + 128)
+constexpr uint32_t kColO = 256;               // O_g: [256 + 128 g, 384 + 128 g)
+
+struct FwdParams {
+    MapAxes aq, ak, av;
+    nvfp4_heads out;
+    float* lse;
+    const int32_t* kv_lens;
+    float c;                                  // scale * log2(e)
+    int H, Hkv, Lq, Lk, d;
+    int group, qtiles, tiles, pairs, items;   // query heads per kv head, tiles of a head, of a kv head, pairs of those
+    int chunks, ring;
+    int* dev_status;
+};
+
+// Work item: sample, kv head, first tile; its key count.
+struct Item {
+    int b, hk, tile, keys, steps;
+    bool two;
+};
+
+__device__ __forceinline__ Item item_of(const FwdParams& p, int it) {
+    Item r;
+    const int bh = it / p.pairs;
+    r.tile = (it - bh * p.pairs) * 2;
+    r.b = bh / p.Hkv;
+    r.hk = bh - r.b * p.Hkv;
+    r.two = r.tile + 1 < p.tiles;
+    r.keys = keys_of(p.kv_lens, r.b, p.Lk);
+    r.steps = (r.keys + kRows - 1) / kRows;
+    return r;
+}
+
+// Head and first query of tile g of an item.
+__device__ __forceinline__ void tile_place(const FwdParams& p, const Item& i, int g, int& head, int& q0) {
+    const int t = i.tile + g, in_group = t / p.qtiles;
+    head = i.hk * p.group + in_group;
+    q0 = (t - in_group * p.qtiles) * kRows;
+}
+
+// The next item at or after `it` (in this CTA's stride) that has keys.
+__device__ __forceinline__ int next_item(const FwdParams& p, int it, Item& item) {
+    for (; it < p.items; it += gridDim.x) {
+        item = item_of(p, it);
+        if (item.steps > 0) break;
+    }
+    return it;
+}
+
+// A ring position and its phase parity.
+struct RingAt {
+    int slot;
+    uint32_t phase;
+    __device__ void advance(int by, int n) {
+        slot += by;
+        if (slot >= n) {
+            slot -= n;
+            phase ^= 1u;
+        }
+    }
+};
+
+__global__ void __launch_bounds__(kThreads, 1)
+xattn_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
+                 const __grid_constant__ CUtensorMap tmap_v, const FwdParams p) {
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ __align__(8) uint64_t q_full[kQBufs], q_empty[kQBufs], kv_full[kMaxRing], kv_empty[kMaxRing];
+    __shared__ __align__(8) uint64_t s_full[2], p_full[2], o_full[2], o_free[2], drain;
+    __shared__ uint32_t tmem_base_sh;
+    __shared__ int abort_sh;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const int tile_bytes = p.chunks * kChunk;
+    uint8_t* ring = smem + kQBufs * tile_bytes;
+    WaitCtx wc{&abort_sh, p.dev_status};
+
+    if (threadIdx.x == 0) {
+        abort_sh = 0;
+        for (int i = 0; i < kQBufs; ++i) {
+            mbar_init(&q_full[i], 1);
+            mbar_init(&q_empty[i], 1);              // the tile's last S product
+        }
+        for (int i = 0; i < kMaxRing; ++i) {
+            mbar_init(&kv_full[i], 1);
+            mbar_init(&kv_empty[i], 1);             // the last product that reads it
+        }
+        for (int g = 0; g < 2; ++g) {
+            mbar_init(&s_full[g], 1);
+            mbar_init(&p_full[g], 4);               // the group's warps
+            mbar_init(&o_full[g], 1);
+            mbar_init(&o_free[g], 4);
+        }
+        mbar_init(&drain, 1);
+        fence_barrier_init();
+        tma_prefetch_desc(&tmap_q);
+        tma_prefetch_desc(&tmap_k);
+        tma_prefetch_desc(&tmap_v);
+    }
+    if (warp == 1) {
+        tmem_alloc(&tmem_base_sh, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_base_sh;
+
+    if (warp < 4) {
+        regs_dec<kRegsLow>();
+        if (warp == 0) {
+            // -------------------------------------------------------- loads, in the order the issuer consumes them
+            RingAt at{0, 0}, qa{0, 0};
+            Item item;
+            bool ok = true;
+            auto load_q = [&](int g) {
+                if (!warp_wait(&q_empty[qa.slot], qa.phase ^ 1u, wc)) return false;
+                if (elect_one()) {
+                    int head, q0;
+                    tile_place(p, item, g, head, q0);
+                    mbar_arrive_expect_tx(&q_full[qa.slot], (uint32_t)tile_bytes);
+                    load_tile(smem + qa.slot * tile_bytes, &tmap_q, &q_full[qa.slot], p.chunks, kChunk, head * p.aq.h, q0,
+                              item.b * p.aq.b);
+                }
+                __syncwarp();
+                qa.advance(1, kQBufs);
+                return true;
+            };
+            auto load_kv = [&](const CUtensorMap* map, const MapAxes& axes, int j) {
+                if (!warp_wait(&kv_empty[at.slot], at.phase ^ 1u, wc)) return false;
+                if (elect_one()) {
+                    mbar_arrive_expect_tx(&kv_full[at.slot], (uint32_t)tile_bytes);
+                    load_tile(ring + at.slot * tile_bytes, map, &kv_full[at.slot], p.chunks, kChunk, item.hk * axes.h,
+                              j * kRows, item.b * axes.b);
+                }
+                __syncwarp();
+                at.advance(1, p.ring);
+                return true;
+            };
+            for (int it = next_item(p, blockIdx.x, item); ok && it < p.items; it = next_item(p, it + gridDim.x, item)) {
+                ok = load_q(0) && load_kv(&tmap_k, p.ak, 0) && (!item.two || load_q(1)) && load_kv(&tmap_v, p.av, 0);
+                for (int j = 1; ok && j < item.steps; ++j) ok = load_kv(&tmap_k, p.ak, j) && load_kv(&tmap_v, p.av, j);
+            }
+            // a block that gave up still waits for its loads in flight
+            if (!ok && lane == 0) {
+                int dummy = 0;
+                WaitCtx w2{&dummy, p.dev_status};
+                RingAt a = at;
+                for (int i = 0; i < p.ring; ++i) {
+                    a.slot = a.slot == 0 ? p.ring - 1 : a.slot - 1;
+                    if (a.slot == p.ring - 1) a.phase ^= 1u;
+                    if (i < p.ring) mbar_wait_limit(&kv_full[a.slot], a.phase, w2, 1000000);
+                }
+                for (int i = 0; i < kQBufs; ++i) mbar_wait_limit(&q_full[i], i < qa.slot ? qa.phase : qa.phase ^ 1u, w2, 1000000);
+            }
+        } else if (warp == 1) {
+            // -------------------------------------------------------- products
+            const uint32_t q_sm = smem_u32(smem), ring_sm = smem_u32(ring);
+            const int dsteps = (p.d + 15) >> 4;
+            const uint32_t idesc_o = idesc_kmn(dsteps * 16);
+            RingAt kat{0, 0}, vat{1, 0};            // K and V tiles alternate in the ring
+            int q_use = 0;                          // running number of Q tiles
+            uint32_t uses[2] = {0, 0}, outs[2] = {0, 0};   // tiles and items of each group so far
+            Item cur, nxt;
+            int q_buf[2] = {0, 0};
+            bool ok = true;
+
+            // S_g of step j of item `i`; the first product on a K tile waits for it, the last frees it
+            auto issue_s = [&](const Item& i, int j, int g) {
+                if (j == 0) {
+                    q_buf[g] = q_use % kQBufs;
+                    if (!warp_wait(&q_full[q_buf[g]], (uint32_t)(q_use / kQBufs) & 1u, wc)) return false;
+                    ++q_use;
+                }
+                if (g == 0 && !warp_wait(&kv_full[kat.slot], kat.phase, wc)) return false;
+                tc_fence_after();
+                if (elect_one()) {
+                    const uint32_t qt = q_sm + q_buf[g] * tile_bytes, kt = ring_sm + kat.slot * tile_bytes;
+                    const int n = min(i.keys - j * kRows, kRows);
+                    const uint32_t idesc = idesc_kk((n + 15) & ~15);
+                    for (int kk = 0; kk < dsteps; ++kk)
+                        tc_mma_bf16(tmem + kColS + g * 128, desc_kmajor(qt, kk, kChunk), desc_kmajor(kt, kk, kChunk), idesc,
+                                    kk != 0 ? 1u : 0u);
+                    tc_commit(&s_full[g]);
+                    if (g == 1 || !i.two) tc_commit(&kv_empty[kat.slot]);
+                    if (j == i.steps - 1) tc_commit(&q_empty[q_buf[g]]);
+                }
+                __syncwarp();
+                if (g == 1 || !i.two) kat.advance(2, p.ring);
+                return true;
+            };
+
+            int it = next_item(p, blockIdx.x, cur);
+            if (it < p.items) ok = issue_s(cur, 0, 0) && (!cur.two || issue_s(cur, 0, 1));
+            while (ok && it < p.items) {
+                const int it2 = next_item(p, it + gridDim.x, nxt);
+                for (int j = 0; ok && j < cur.steps; ++j) {
+                    const bool last = j == cur.steps - 1;
+                    const bool more = !last || it2 < p.items;
+                    const Item& ni = last ? nxt : cur;          // the step whose S comes next
+                    const int nj = last ? 0 : j + 1;
+                    const int n = min(cur.keys - j * kRows, kRows);
+                    for (int g = 0; ok && g < (cur.two ? 2 : 1); ++g) {
+                        ok = warp_wait(&p_full[g], uses[g] & 1u, wc) &&
+                             (g == 1 || warp_wait(&kv_full[vat.slot], vat.phase, wc)) &&
+                             // the item's first product overwrites O_g: the previous one's has been read out
+                             (j > 0 || outs[g] == 0 || warp_wait(&o_free[g], (outs[g] - 1) & 1u, wc));
+                        if (!ok) break;
+                        ++uses[g];
+                        const uint32_t vt = ring_sm + vat.slot * tile_bytes;
+                        if (g == 0 && (n & 15) != 0 && cur.keys < p.Lk) {
+                            // values past the sample's length meet P = 0, but may be NaN: the rest
+                            // of the last 16 rows reads as zeros (rows past the tensor already do)
+                            uint8_t* vrow = ring + vat.slot * tile_bytes;
+                            const int rows = 16 - (n & 15);
+                            for (int i = lane; i < rows * 8 * p.chunks; i += 32) {
+                                const int c = i / (rows * 8), r = i - c * rows * 8;
+                                *reinterpret_cast<uint4*>(vrow + c * kChunk + n * 128 + r * 16) = make_uint4(0, 0, 0, 0);
+                            }
+                            fence_proxy_async_smem();
+                            __syncwarp();
+                        }
+                        tc_fence_after();
+                        if (elect_one()) {
+                            const int ksteps = (n + 15) >> 4;
+                            for (int kk = 0; kk < ksteps; ++kk)
+                                tc_mma_bf16_ta(tmem + kColO + g * 128, tmem + kColS + g * 128 + kk * 8,
+                                               desc_mnmajor(vt, kk, kChunk), idesc_o, (j | kk) != 0 ? 1u : 0u);
+                            if (g == 1 || !cur.two) tc_commit(&kv_empty[vat.slot]);
+                            if (last) tc_commit(&o_full[g]);
+                        }
+                        __syncwarp();
+                        if (last) ++outs[g];
+                        if (more && (g == 0 || ni.two)) ok = issue_s(ni, nj, g);
+                    }
+                    if (ok && more && ni.two && !cur.two) ok = issue_s(ni, nj, 1);
+                    vat.advance(2, p.ring);
+                }
+                it = it2;
+                cur = nxt;
+            }
+            if (elect_one()) tc_commit(&drain);
+            __syncwarp();
+            int dummy = 0;
+            WaitCtx w2{&dummy, p.dev_status};
+            mbar_wait(&drain, 0, w2);
+        }
+    } else {
+        regs_inc<kRegsHigh>();
+        // ------------------------------------------------------------ softmax and output of tile g
+        const int g = (warp - 4) >> 2, quarter = warp & 3, r = quarter * 32 + lane;
+        const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
+        const uint32_t ts = tmem + lane_base + kColS + g * 128, to = tmem + lane_base + kColO + g * 128;
+        const int ochunks = (p.d + 31) >> 5;
+        uint32_t uses = 0, outs = 0;
+        bool ok = true;
+        for (int it = blockIdx.x; ok && it < p.items; it += gridDim.x) {
+            const Item item = item_of(p, it);
+            if (g == 1 && !item.two) continue;
+            float m = -INFINITY, l = 0.0f;
+            for (int j = 0; j < item.steps; ++j, ++uses) {
+                if (!warp_wait(&s_full[g], uses & 1u, wc)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const int n = min(item.keys - j * kRows, kRows);
+                uint32_t v[kRows];
+                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                if (n == kRows) {
+#pragma unroll
+                    for (int c4 = 0; c4 < 4; ++c4)
+                        tmem_ld_32x32b_x32(ts + c4 * 32, *reinterpret_cast<uint32_t(*)[32]>(&v[c4 * 32]));
+                    tmem_ld_wait();
+                } else {
+#pragma unroll
+                    for (int c4 = 0; c4 < 4; ++c4)
+                        if (c4 * 32 < n) tmem_ld_32x32b_x32(ts + c4 * 32, *reinterpret_cast<uint32_t(*)[32]>(&v[c4 * 32]));
+                    tmem_ld_wait();
+                    // keys past the length: -infinity whatever was computed there
+#pragma unroll
+                    for (int i = 0; i < kRows; ++i)
+                        if (i >= n) v[i] = 0xFF800000u;
+                }
+#pragma unroll
+                for (int i = 0; i < kRows; ++i) mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(v[i]));
+                const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.c;
+                const bool move = mt > m + 8.0f;
+                const float mref = move ? mt : m;
+                const float alpha = move ? ex2(m - mt) : 1.0f;
+                float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int c2 = 0; c2 < 2; ++c2) {
+                    if (c2 * 64 >= n) break;
+                    uint32_t w[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        const float e0 = ex2(fmaf(__uint_as_float(v[c2 * 64 + 2 * i]), p.c, -mref));
+                        const float e1 = ex2(fmaf(__uint_as_float(v[c2 * 64 + 2 * i + 1]), p.c, -mref));
+                        sum[i & 3] += e0 + e1;
+                        w[i] = pack_bf16(e0, e1);
+                    }
+                    tmem_st_x32(ts + c2 * 32, w);
+                }
+                l = fmaf(l, alpha, (sum[0] + sum[1]) + (sum[2] + sum[3]));
+                m = mref;
+                // O_g rescaled: its previous product is done, for S_g came after it
+                if (j >= 1 && __any_sync(0xffffffffu, alpha != 1.0f)) {
+                    for (int c4 = 0; c4 < ochunks; ++c4) {
+                        uint32_t o[32];
+                        tmem_ld_32x32b_x32(to + c4 * 32, o);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+                        tmem_st_x32(to + c4 * 32, o);
+                    }
+                }
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_full[g]);
+            }
+            if (!ok) break;
+            int head, q0;
+            tile_place(p, item, g, head, q0);
+            const int row = q0 + r;
+            uint16_t* orow = static_cast<uint16_t*>(p.out.data) + (int64_t)item.b * p.out.batch_stride +
+                             (int64_t)row * p.out.token_stride + (int64_t)head * p.out.head_stride;
+            if (p.lse && row < p.Lq)
+                p.lse[((int64_t)item.b * p.H + head) * p.Lq + row] = item.steps > 0 ? (m + log2f(l)) * kLn2 : -INFINITY;
+            if (item.steps == 0) {
+                if (row < p.Lq)
+                    for (int i = 0; i < p.d; i += 8) *reinterpret_cast<uint4*>(orow + i) = make_uint4(0, 0, 0, 0);
+                continue;
+            }
+            if (!warp_wait(&o_full[g], outs & 1u, wc)) break;
+            ++outs;
+            tc_fence_after();
+            const float inv = __frcp_rn(l);
+            for (int c4 = 0; c4 < ochunks; ++c4) {
+                uint32_t o[32];
+                tmem_ld_32x32b_x32(to + c4 * 32, o);
+                tmem_ld_wait();
+                if (c4 == ochunks - 1) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&o_free[g]);
+                }
+                if (row < p.Lq) {
+#pragma unroll
+                    for (int i = 0; i < 32; i += 8) {
+                        if (c4 * 32 + i >= p.d) break;
+                        uint32_t w[4];
+#pragma unroll
+                        for (int u = 0; u < 4; ++u)
+                            w[u] = pack_bf16(__uint_as_float(o[i + 2 * u]) * inv, __uint_as_float(o[i + 2 * u + 1]) * inv);
+                        *reinterpret_cast<uint4*>(orow + c4 * 32 + i) = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                }
+            }
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+cudaError_t launch_forward_tiles(const CrossAttnArgs& a, int num_sms, cudaStream_t stream) {
+    FwdParams p{};
+    CUtensorMap mq, mk, mv;
+    if (a.Lk > 0) {
+        if (!make_heads_map(&mq, a.q, a.B, a.Lq, a.H, a.d, kRows, &p.aq) ||
+            !make_heads_map(&mk, a.k, a.B, a.Lk, a.Hkv, a.d, kRows, &p.ak) ||
+            !make_heads_map(&mv, a.v, a.B, a.Lk, a.Hkv, a.d, kRows, &p.av))
+            return cudaErrorInvalidValue;
+    } else {
+        mq = mk = mv = CUtensorMap{};               // no item has keys: nothing is loaded
+    }
+    p.out = a.out;
+    p.lse = a.lse;
+    p.kv_lens = a.kv_lens;
+    p.c = a.scale * kLog2e;
+    p.H = a.H;
+    p.Hkv = a.Hkv;
+    p.Lq = a.Lq;
+    p.Lk = a.Lk;
+    p.d = a.d;
+    p.group = a.H / a.Hkv;
+    p.qtiles = (a.Lq + kRows - 1) / kRows;
+    p.tiles = p.group * p.qtiles;
+    p.pairs = (p.tiles + 1) / 2;
+    p.items = a.B * a.Hkv * p.pairs;
+    p.chunks = (a.d + 63) / 64;
+    const int tile_bytes = p.chunks * kChunk;
+    p.ring = (kSmemLimit - 1024 - 1024 - kQBufs * tile_bytes) / tile_bytes;
+    if (p.ring > kMaxRing) p.ring = kMaxRing;
+    p.dev_status = a.dev_status;
+    const int smem = (kQBufs + p.ring) * tile_bytes + 1024;
+    cudaError_t e = cudaFuncSetAttribute(xattn_fwd_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    xattn_fwd_kernel<<<p.items < num_sms ? p.items : num_sms, kThreads, smem, stream>>>(mq, mk, mv, p);
+    e = cudaGetLastError();
+    if (e == cudaSuccess) count_launch(1);
+    return e;
+}
+
+}  // namespace xattn
+
+cudaError_t launch_cross_attention(const CrossAttnArgs& a, int num_sms, cudaStream_t stream) {
+    return xattn::launch_forward_tiles(a, num_sms, stream);
+}
+
+}  // namespace nvfp4
