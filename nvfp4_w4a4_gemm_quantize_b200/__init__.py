@@ -26,12 +26,14 @@ Convenience (allocate outputs with torch, then call the above):
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
+import struct
 from dataclasses import dataclass
 
 import torch
 
-from ._lib import MAX_GROUP, NVFP4Error, NVFP4GemmProblem, NVFP4Heads, check, lib  # noqa: F401
+from ._lib import MAX_GROUP, NVFP4Error, NVFP4GemmProblem, check, lib  # noqa: F401
 
 NVFP4_DTYPE_BF16 = 0
 NVFP4_DTYPE_F32 = 1
@@ -61,7 +63,8 @@ def _ptr(t) -> int | None:
 
 def _stream(stream) -> int | None:
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        # the current stream's handle without building a Stream object (3 us of host time a call)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -214,14 +217,20 @@ def nvfp4_gemm_w4a16(x, w_codes, w_sf, w_scale, M, N, K, y, y_dtype=NVFP4_DTYPE_
     check(st, "nvfp4_gemm_w4a16")
 
 
-def _heads(t) -> NVFP4Heads | None:
-    """A [batch, tokens, heads, d] tensor (d contiguous) as nvfp4_heads."""
-    if t is None:
-        return None
+_PACK_HEADS = struct.Struct("Pqqq").pack
+
+
+def _heads(t) -> bytes:
+    """A [batch, tokens, heads, d] CUDA tensor (d contiguous) as nvfp4_heads."""
     if not t.is_cuda:
         raise ValueError("tensor must live on a CUDA device")
     sb, sl, sh, _ = t.stride()
-    return NVFP4Heads(t.data_ptr(), sb, sl, sh)
+    return _PACK_HEADS(t.data_ptr(), sb, sl, sh)
+
+
+@functools.lru_cache(maxsize=64)
+def _ints(values: tuple) -> bytes:
+    return struct.pack(f"{len(values)}i", *values)
 
 
 def nvfp4_gemv_w4a16(x, ld_x, w_codes, w_sf, w_scale, w_format, bias, M, N, K, y, y_dtype=NVFP4_DTYPE_BF16,
@@ -233,18 +242,17 @@ def nvfp4_gemv_w4a16(x, ld_x, w_codes, w_sf, w_scale, w_format, bias, M, N, K, y
 def nvfp4_rotary(x, positions, pos_dtype, pos_batch_stride, pos_token_stride, axis_dims, theta, B, L, H, d, dtype,
                  flags, out, stream=None) -> None:
     """``x`` and ``out``: [B, L, H, d] tensors; ``axis_dims``: a sequence of ints."""
-    dims = (ctypes.c_int * len(axis_dims))(*axis_dims)
-    check(lib().nvfp4_rotary(ctypes.byref(_heads(x)), _ptr(positions), pos_dtype, pos_batch_stride, pos_token_stride,
-                             dims, len(axis_dims), theta, B, L, H, d, dtype, flags, ctypes.byref(_heads(out)),
+    check(lib().nvfp4_rotary(_heads(x), _ptr(positions), pos_dtype, pos_batch_stride, pos_token_stride,
+                             _ints(tuple(axis_dims)), len(axis_dims), theta, B, L, H, d, dtype, flags, _heads(out),
                              _stream(stream)), "nvfp4_rotary")
 
 
 def nvfp4_cross_attention(q, k, v, kv_lens, scale, B, H, Hkv, Lq, Lk, d, out, lse, dev_status=None,
                           stream=None) -> None:
     """``q``, ``k``, ``v``, ``out``: [batch, tokens, heads, d] tensors."""
-    check(lib().nvfp4_cross_attention(*(ctypes.byref(_heads(t)) for t in (q, k, v)), _ptr(kv_lens), scale, B, H, Hkv,
-                                      Lq, Lk, d, ctypes.byref(_heads(out)), _ptr(lse), _ptr(dev_status),
-                                      _stream(stream)), "nvfp4_cross_attention")
+    check(lib().nvfp4_cross_attention(_heads(q), _heads(k), _heads(v), _ptr(kv_lens), scale, B, H, Hkv, Lq, Lk, d,
+                                      _heads(out), _ptr(lse), _ptr(dev_status), _stream(stream)),
+          "nvfp4_cross_attention")
 
 
 def nvfp4_cross_attention_backward_workspace_bytes(B: int, H: int, Hkv: int, Lq: int, Lk: int, d: int) -> int:
@@ -254,8 +262,8 @@ def nvfp4_cross_attention_backward_workspace_bytes(B: int, H: int, Hkv: int, Lq:
 def nvfp4_cross_attention_backward(grad_out, q, k, v, out, lse, kv_lens, scale, B, H, Hkv, Lq, Lk, d, dq, dk, dv,
                                    workspace, workspace_bytes, dev_status=None, stream=None) -> None:
     check(lib().nvfp4_cross_attention_backward(
-        *(ctypes.byref(_heads(t)) for t in (grad_out, q, k, v, out)), _ptr(lse), _ptr(kv_lens), scale, B, H, Hkv, Lq,
-        Lk, d, *(ctypes.byref(_heads(t)) for t in (dq, dk, dv)), _ptr(workspace), workspace_bytes, _ptr(dev_status),
+        _heads(grad_out), _heads(q), _heads(k), _heads(v), _heads(out), _ptr(lse), _ptr(kv_lens), scale, B, H, Hkv,
+        Lq, Lk, d, _heads(dq), _heads(dk), _heads(dv), _ptr(workspace), workspace_bytes, _ptr(dev_status),
         _stream(stream)), "nvfp4_cross_attention_backward")
 
 
@@ -536,17 +544,19 @@ def _require(ok: bool, what: str) -> None:
 
 def _on_device(*tensors) -> None:
     """Every given tensor lives on the current CUDA device, where the kernels run."""
-    here = torch.cuda.current_device() if torch.cuda.is_available() else None
+    here = None
     for t in tensors:
-        if t is not None:
-            _require(t.is_cuda and t.device.index == here, f"tensor on {t.device}: the call runs on the current CUDA device")
+        if t is None:
+            continue
+        if t.is_cuda and here is None:
+            here = torch.cuda.current_device()
+        if not t.is_cuda or t.get_device() != here:
+            raise ValueError(f"tensor on {t.device}: the call runs on the current CUDA device")
 
 
 def _used_on(stream, *tensors) -> None:
     """Tensors a call allocated (on the current stream) stay unrecycled until
     the other stream the call runs on has passed."""
-    if stream is None:
-        return
     s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
     if s != torch.cuda.current_stream():
         for t in tensors:
@@ -559,7 +569,7 @@ def gemv_w4a16(x: torch.Tensor, w: NVFP4Tensor | MXTensor, bias: torch.Tensor | 
     (rows may be strided), W NVFP4 or MX [N, K], bias FP32 [N], Y bf16 or FP32."""
     mx = isinstance(w, MXTensor)
     _require(x.dtype == torch.bfloat16 and x.dim() == 2 and x.shape[1] == w.k, "x must be bf16 [M, w.k]")
-    _require(x.shape[0] <= NVFP4_GEMV_MAX_ROWS, f"at most {NVFP4_GEMV_MAX_ROWS} rows: gemm_w4a16 takes more")
+    _require(x.shape[0] <= NVFP4_GEMV_MAX_ROWS, "at most NVFP4_GEMV_MAX_ROWS rows: gemm_w4a16 takes more")
     _require(x.stride(1) == 1, "x must be contiguous along k")
     _require(bias is None or (bias.dtype == torch.float32 and bias.shape == (w.rows,) and bias.is_contiguous()),
              "bias must be a contiguous FP32 [N]")
@@ -569,7 +579,7 @@ def gemv_w4a16(x: torch.Tensor, w: NVFP4Tensor | MXTensor, bias: torch.Tensor | 
     _on_device(x, w.codes, w.sf, None if mx else w.scale, bias, y)
     nvfp4_gemv_w4a16(x, max(x.stride(0), w.k), w.codes, w.sf, None if mx else w.scale,
                      NVFP4_WEIGHTS_MX if mx else NVFP4_WEIGHTS_NVFP4, bias, M, w.rows, w.k, y, _DT[y.dtype], stream)
-    if out is None:
+    if out is None and stream is not None:
         _used_on(stream, y)
     return y
 
@@ -595,20 +605,21 @@ def rotary(x: torch.Tensor, positions: torch.Tensor, axes, theta: float = 10000.
     rows quantize() takes), or x itself."""
     _require(x.dim() == 4 and x.dtype in _DT and x.stride(3) == 1, "x must be bf16 or FP32 [B, L, H, d], d contiguous")
     B, L, H, d = x.shape
-    axes = tuple(int(a) for a in axes)
-    _require(positions.dtype in (torch.int32, torch.float32) and positions.dim() in (2, 3)
-             and tuple(positions.shape[-2:]) == (L, len(axes)) and (positions.dim() == 2 or positions.shape[0] in (1, B)),
+    axes = tuple(axes)
+    ps, pt = positions.shape, positions.stride()
+    per_sample = len(ps) == 3 and ps[0] > 1
+    _require(positions.dtype in (torch.int32, torch.float32) and len(ps) in (2, 3) and ps[-2] == L
+             and ps[-1] == len(axes) and (len(ps) == 2 or ps[0] in (1, B)),
              "positions must be int32 or FP32 [L, n_axes] or [B, L, n_axes]")
-    _require(positions.stride(-1) == 1 or len(axes) == 1, "positions must be contiguous along the axes")
+    _require(pt[-1] == 1 or len(axes) == 1, "positions must be contiguous along the axes")
     y = out if out is not None else torch.empty(B, L, H, d, dtype=x.dtype, device=x.device)
     _require(y.dtype == x.dtype and y.shape == x.shape and y.stride(3) == 1, "out must match x, d contiguous")
     _on_device(x, positions, y)
     flags = (NVFP4_ROTARY_INTERLEAVED if interleaved else 0) | (NVFP4_ROTARY_INVERSE if inverse else 0)
-    per_sample = positions.dim() == 3 and positions.shape[0] > 1
     nvfp4_rotary(x, positions, NVFP4_POSITION_I32 if positions.dtype == torch.int32 else NVFP4_POSITION_F32,
-                 positions.stride(0) if per_sample else 0, positions.stride(-2), axes, float(theta), B, L, H, d,
+                 pt[0] if per_sample else 0, pt[-2], axes, float(theta), B, L, H, d,
                  _DT[x.dtype], flags, y, stream)
-    if out is None:
+    if out is None and stream is not None:
         _used_on(stream, y)
     return y
 
@@ -633,8 +644,8 @@ class RotaryEmbedding(torch.autograd.Function):
 
 def _attention_sizes(q, k, v, kv_lens):
     for t in (q, k, v):
-        _require(t.dim() == 4 and t.dtype == torch.bfloat16 and t.stride(3) == 1,
-                 "q, k and v must be bf16 [batch, tokens, heads, d], d contiguous")
+        if t.dim() != 4 or t.dtype is not torch.bfloat16 or t.stride(3) != 1:
+            raise ValueError("q, k and v must be bf16 [batch, tokens, heads, d], d contiguous")
     B, Lq, H, d = q.shape
     Lk, Hkv = k.shape[1], k.shape[2]
     _require(k.shape == (B, Lk, Hkv, d) and v.shape == k.shape, "k and v must be [B, Lk, Hkv, d] of q's B and d")
@@ -659,7 +670,7 @@ def cross_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, kv_lens: 
     nvfp4_cross_attention(q, k, v, kv_lens, 1.0 / math.sqrt(d) if scale is None else float(scale), *sizes, o, lse,
                           dev_status, stream)
     if stream is not None:
-        _used_on(stream, *(t for t in (o if out is None else None, lse) if t is not None))
+        _used_on(stream, *([o] if out is None else []), *([lse] if return_lse else []))
     return (o, lse) if return_lse else o
 
 

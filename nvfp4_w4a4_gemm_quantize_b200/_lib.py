@@ -36,12 +36,6 @@ class NVFP4GemmProblem(ctypes.Structure):
 
 MAX_GROUP = 8
 
-
-class NVFP4Heads(ctypes.Structure):
-    """nvfp4_heads (include/nvfp4_dit.h): a [batch, tokens, heads, d] operand."""
-    _fields_ = [("data", _p), ("batch_stride", _i64), ("token_stride", _i64), ("head_stride", _i64)]
-
-
 # every symbol include/nvfp4.h and include/nvfp4_dit.h declare, with (restype, argtypes)
 SIGNATURES = {
     "nvfp4_sf_bytes": (ctypes.c_size_t, [_i64, _i64]),

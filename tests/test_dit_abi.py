@@ -4,6 +4,7 @@ each call fails its checks, or has nothing to do, before touching the device).""
 import ctypes
 import os
 import re
+import struct
 
 import pytest
 import torch
@@ -55,7 +56,7 @@ def test_gemv_rejects_bad_arguments(L, bad, want):
 
 
 def heads(data=A, sb=1 << 20, sl=2048, sh=128):
-    return ctypes.byref(_lib.NVFP4Heads(data, sb, sl, sh))
+    return struct.pack("Pqqq", data or 0, sb, sl, sh)            # nvfp4_heads
 
 
 def rotary(L, x=heads(), pos=A, pt=0, pb=0, pl=3, axes=(44, 42, 42), theta=1e4, B=2, T=16, H=4, d=128, dt=0, flags=1,
