@@ -78,6 +78,13 @@ nvfp4_status device_ok(int* sms) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return NVFP4_ERR_CUDA;
     if (dev < 0 || dev >= 64) return NVFP4_ERR_UNSUPPORTED_DEVICE;
+    // a thread that made no CUDA call yet (an autograd worker) has no current
+    // context, which encoding a tensor map needs
+    static thread_local int bound = -1;
+    if (bound != dev) {
+        if (cudaSetDevice(dev) != cudaSuccess) return NVFP4_ERR_CUDA;
+        bound = dev;
+    }
     DevInfo& d = g_dev[dev];
     if (d.checked == 0) {
         int major = 0, minor = 0, n = 0;

@@ -16,8 +16,12 @@ Bounds per element, from the inputs in FP64 (h = 2^-8, the half step of bf16):
   dS: P scale (h |dP - D| + 3 e |dP - D| + 2^-18 (|grad| |v|) + error of D), D
     from the rounded out: sum |grad| * (error of out) + 2^-18 sum |grad out|
     (sums over d <= 128: at most 16 steps);
-  dq, dk: the errors of dS times |k|, |q|, plus f |dS| |k| ..., plus h |dq|."""
+  dq, dk: the errors of dS times |k|, |q|, plus f |dS| |k| ..., plus h |dq|;
+  in the gradients P = exp(scale q k - lse) comes out as zero where it is below
+    the least normal number u = 2^-126 (the hardware exponential flushes it):
+    at most u off, so u more in every P of dv, u scale |dP - D| more in dS."""
 import math
+import threading
 
 import pytest
 import torch
@@ -26,7 +30,7 @@ import nvfp4_w4a4_gemm_quantize_b200 as nv
 
 pytestmark = pytest.mark.gpu
 
-H8, F = 2.0 ** -8, 2.0 ** -18
+H8, F, U = 2.0 ** -8, 2.0 ** -18, 2.0 ** -126
 
 
 def _inputs(B, Lq, Lk, H, Hkv, d, seed=0, std=1.0):
@@ -65,6 +69,7 @@ def _reference(q, k, v, lens, scale, do=None):
         eD = (g.abs() * tol).sum(3, keepdim=True) + F * (g * out).abs().sum(3, keepdim=True)
         ds = p * (dp - D) * scale
         eds = p * scale * ((H8 + 3 * e) * (dp - D).abs() + F * (g.abs() @ vd.abs().transpose(2, 3)) + eD)
+        eds = eds + torch.where(keep[:, None, None], U * scale * (dp - D).abs(), 0.0)
 
         def shared(t):                       # [B, H, Lk, d] summed over the heads that share a key
             return t.reshape(B, Hkv, G, Lk, d).sum(2).transpose(1, 2)
@@ -72,7 +77,7 @@ def _reference(q, k, v, lens, scale, do=None):
         dq, dk, dv = ds @ kd, shared(ds.transpose(2, 3) @ qd), shared(p.transpose(2, 3) @ g)
         edq = eds @ kd.abs() + fk * (ds.abs() @ kd.abs()) + H8 * dq.abs()
         edk = shared(eds.transpose(2, 3) @ qd.abs() + fq * (ds.abs().transpose(2, 3) @ qd.abs())) + H8 * dk.abs()
-        edv = shared(((H8 + 3 * e + fq) * p).transpose(2, 3) @ g.abs()) + H8 * dv.abs()
+        edv = shared((torch.where(keep[:, None, None], U, 0.0) + (H8 + 3 * e + fq) * p).transpose(2, 3) @ g.abs()) + H8 * dv.abs()
         res |= {"dq": (dq.transpose(1, 2), edq.transpose(1, 2)), "dk": (dk, edk), "dv": (dv, edv)}
     return res
 
@@ -309,6 +314,22 @@ def test_block_sizes(cuda_ok, B, Lq, Lk, H, d, lens):
     """Image and video blocks: many work items a CTA, both passes."""
     q, k, v, do = _inputs(B, Lq, Lk, H, H, d, seed=13)
     _check(q, k, v, lens, do=do)
+
+
+def test_calls_from_new_threads(cuda_ok):
+    """The first CUDA call of a thread (as in an autograd worker)."""
+    q, k, v, do = _inputs(1, 130, 40, 2, 2, 64, seed=16)
+    out, lse = nv.cross_attention(q, k, v, return_lse=True)
+    want = nv.cross_attention_backward(do, q, k, v, out, lse)
+    got, buf = [], torch.empty_like(out)
+    torch.cuda.synchronize()
+    for call in (lambda: nv.cross_attention(q, k, v, out=buf),
+                 lambda: got.extend(nv.cross_attention_backward(do, q, k, v, out, lse))):
+        t = threading.Thread(target=call)
+        t.start()
+        t.join()
+    torch.cuda.synchronize()
+    assert torch.equal(buf, out) and len(got) == 3 and all(torch.equal(a, b) for a, b in zip(got, want))
 
 
 @pytest.mark.parametrize("Lq", [1, 300])
