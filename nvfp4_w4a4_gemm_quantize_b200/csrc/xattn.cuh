@@ -30,17 +30,19 @@ struct MapAxes {
     int b, h;
 };
 
-// A [B, L, H, d] bf16 operand as a 4-D map (d, h, l, b) with boxes of 64 columns x `rows` tokens of one head.
-inline bool make_heads_map(CUtensorMap* map, const nvfp4_heads& t, int B, int L, int H, int d, int rows, MapAxes* axes) {
+// A [B, L, H, d] bf16 operand as a 4-D map (d, h, l, b) with boxes of `cols` (64 or 32: the swizzle is as wide as
+// their bytes) x `rows` tokens of one head.
+inline bool make_heads_map(CUtensorMap* map, const nvfp4_heads& t, int B, int L, int H, int d, int rows, MapAxes* axes,
+                           int cols = 64) {
     axes->b = t.batch_stride != 0;
     axes->h = t.head_stride != 0;
     const uint64_t step = (uint64_t)d * 2;   // a legal stride for axes of one element
     const uint64_t dims[4] = {(uint64_t)d, axes->h ? (uint64_t)H : 1u, (uint64_t)L, axes->b ? (uint64_t)B : 1u};
     const uint64_t strides[3] = {axes->h ? (uint64_t)t.head_stride * 2 : step, L > 1 ? (uint64_t)t.token_stride * 2 : step,
                                  axes->b ? (uint64_t)t.batch_stride * 2 : step};
-    const uint32_t box[4] = {64, 1, (uint32_t)rows, 1};
-    return make_tmap_4d(map, t.data, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B) ==
-           CUDA_SUCCESS;
+    const uint32_t box[4] = {(uint32_t)cols, 1, (uint32_t)rows, 1};
+    return make_tmap_4d(map, t.data, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, dims, strides, box,
+                        cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B) == CUDA_SUCCESS;
 }
 
 // Valid keys of sample b.
@@ -55,21 +57,17 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, u
         : "memory");
 }
 
+// A box from shared memory; rows and columns past the tensor are not written.
+__device__ __forceinline__ void tma_store_4d(const CUtensorMap* map, const void* src, int x, int h, int l, int b) {
+    asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.bulk_group [%0, {%2, %3, %4, %5}], [%1];"
+                 ::"l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(src)), "r"(x), "r"(h), "r"(l), "r"(b)
+                 : "memory");
+}
+
 // A tile (all its 64-column chunks), completion on `bar` (which expects chunks * rows * 128 bytes).
 __device__ __forceinline__ void load_tile(uint8_t* dst, const CUtensorMap* map, uint64_t* bar, int chunks, int chunk_bytes,
                                           int h, int l, int b) {
     for (int c = 0; c < chunks; ++c) tma_load_4d(dst + c * chunk_bytes, map, bar, c * 64, h, l, b);
-}
-
-// D[tmem] (+)= A[tmem] * B[smem], bf16, A packed two values a column.
-__device__ __forceinline__ void tc_mma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
-                                               uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
-        ::"r"(d_tmem), "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
-        : "memory");
 }
 
 // kind::f16 on bf16 operands, FP32 sums: both K-major (idesc_bf16), or B
@@ -77,13 +75,83 @@ __device__ __forceinline__ void tc_mma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem,
 __device__ __forceinline__ uint32_t idesc_kk(int N) { return idesc_bf16(kRows, N); }
 __device__ __forceinline__ uint32_t idesc_kmn(int N) { return idesc_bf16(kRows, N) | (1u << 16); }
 
-// A tile as a K-major operand (k = d), step kk: 16 columns on; chunks of `chunk_bytes`.
-__device__ __forceinline__ uint64_t desc_kmajor(uint32_t tile, int kk, int chunk_bytes) {
-    return sdesc_kmajor_sw128(tile + (kk >> 2) * chunk_bytes + (kk & 3) * 32);
+// Products of a tile, at most eight steps of 16 along k, called by a converged
+// warp; each instruction elects the lane that issues it.  (A tile product takes
+// the tensor core 512 cycles.  Issued like this, eight steps take 436 cycles of
+// the warp; behind one elected branch 540; under a predicate on the lane number,
+// which may hold for several lanes as far as the compiler knows, 770 and more.)
+// The descriptors of the steps differ by constants in their low word.
+constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);   // 8-row groups 1024 bytes apart, 128-byte swizzle
+
+// D[tmem] = A B^T: both tiles K-major (k = d: four steps a chunk).
+__device__ __forceinline__ void product_kk(uint32_t d, uint32_t a_tile, uint32_t b_tile, uint32_t idesc, int steps) {
+    const uint32_t a = (a_tile >> 4) | (1u << 16), b = (b_tile >> 4) | (1u << 16);
+#pragma unroll
+    for (int kk = 0; kk < 8; ++kk) {
+        if (kk >= steps) break;
+        const uint32_t off = (kk >> 2) * (kChunk >> 4) + (kk & 3) * 2;
+        asm volatile(
+            "{\n\t.reg .pred p, q;\n\t.reg .b64 da, db;\n\t"
+            "mov.b64 da, {%1, %3};\n\tmov.b64 db, {%2, %3};\n\t"
+            "setp.ne.b32 p, %5, 0;\n\telect.sync _|q, 0xffffffff;\n\t"
+            "@q tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, p;\n\t}"
+            ::"r"(d), "r"(a + off), "r"(b + off), "n"(kDescHigh), "r"(idesc), "r"((uint32_t)kk)
+            : "memory");
+    }
 }
-// A tile as an MN-major B operand (k = its rows, n = d), step kk: 16 rows on.
-__device__ __forceinline__ uint64_t desc_mnmajor(uint32_t tile, int kk, int chunk_bytes) {
-    return make_sdesc(tile + kk * 2048, chunk_bytes, 1024, 2);
+
+// D[tmem] (+)= A B: A packed in TMEM, two values a column, the 16 values of step
+// kk at a + (kk / GROUP) * 16 GROUP + (kk % GROUP) * 8; B MN-major (k = its rows).
+template <int GROUP>
+__device__ __forceinline__ void product_tmem(uint32_t d, uint32_t a, uint32_t b_tile, uint32_t idesc, int steps,
+                                             bool accumulate) {
+    const uint32_t b = (b_tile >> 4) | ((uint32_t)(kChunk >> 4) << 16);
+#pragma unroll
+    for (int kk = 0; kk < 8; ++kk) {
+        if (kk >= steps) break;
+        asm volatile(
+            "{\n\t.reg .pred p, q;\n\t.reg .b64 db;\n\t"
+            "mov.b64 db, {%2, %3};\n\t"
+            "setp.ne.b32 p, %5, 0;\n\telect.sync _|q, 0xffffffff;\n\t"
+            "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %4, p;\n\t}"
+            ::"r"(d), "r"(a + (kk / GROUP) * 16 * GROUP + (kk % GROUP) * 8), "r"(b + kk * 128), "n"(kDescHigh), "r"(idesc),
+              "r"(kk > 0 || accumulate ? 1u : 0u)
+            : "memory");
+    }
+}
+
+// What the issuing warp has to know of a step, left by the loading warp beside
+// the step's K tile (0: no more steps).
+constexpr uint32_t kInfoKeys = 0xFFu;        // keys of the tile, 1 .. 128
+constexpr uint32_t kInfoFirst = 1u << 8;     // first, last step of an item
+constexpr uint32_t kInfoLast = 1u << 9;
+constexpr uint32_t kInfoZero = 1u << 10;     // rows past the sample's length may hold anything
+constexpr uint32_t kInfoTwo = 1u << 11;      // the item has a second query tile
+
+__device__ __forceinline__ uint32_t step_info(int keys, int Lk, int j, int steps, bool two) {
+    const int n = min(keys - j * kRows, kRows);
+    return (uint32_t)n | (j == 0 ? kInfoFirst : 0u) | (j == steps - 1 ? kInfoLast : 0u) |
+           ((n & 15) != 0 && keys < Lk ? kInfoZero : 0u) | (two ? kInfoTwo : 0u);
+}
+
+// Rows [n, n rounded up to 16) of a tile as zeros, by the whole warp: those keys
+// meet a zero in the other operand, but may be NaN (rows past the tensor are zeros already).
+__device__ __forceinline__ void zero_rest(uint8_t* tile, int n, int chunks, int lane) {
+    const int pieces = (16 - (n & 15)) * 8;
+    for (int c = 0; c < chunks; ++c)
+        for (int i = lane; i < pieces; i += 32)
+            *reinterpret_cast<uint4*>(tile + c * kChunk + n * 128 + i * 16) = make_uint4(0, 0, 0, 0);
+    fence_proxy_async_smem();
+    __syncwarp();
+}
+
+// `bar` is told when all products issued so far are complete (a converged warp).
+__device__ __forceinline__ void commit(uint64_t* bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}"
+        ::"r"(smem_u32(bar))
+        : "memory");
 }
 
 __device__ __forceinline__ void tmem_st_x32(uint32_t taddr, const uint32_t (&r)[32]) {
@@ -116,6 +184,36 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
+}
+
+// Two FP32 operations in one instruction, on neighbouring registers.
+struct F2 {
+    float x, y;
+};
+__device__ __forceinline__ uint64_t f2_bits(float x, float y) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ F2 f2_of(uint64_t b) {
+    F2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(b));
+    return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(f2_bits(a.x, a.y)), "l"(f2_bits(b.x, b.y)), "l"(f2_bits(c.x, c.y)));
+    return f2_of(r);
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(f2_bits(a.x, a.y)), "l"(f2_bits(b.x, b.y)));
+    return f2_of(r);
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(f2_bits(a.x, a.y)), "l"(f2_bits(b.x, b.y)));
+    return f2_of(r);
 }
 
 // The whole warp waits; false once the block gives up.

@@ -14,23 +14,26 @@
 // issuing warp starts dP of the next step, dS K of this one and S of the one
 // after next: the exponentials of the next step run meanwhile on an S that is
 // there already.  The order runs on across work items; dQ of an item is read
-// out between the next item's exponentials and its dS.
+// out between the next item's exponentials and its dS, and goes out by TMA from
+// its own dO tile.
 // dK, dV (dkv_kernel): a block has one key tile and a range of the query tiles
 // of the heads that share it.  S and dP are computed transposed, so that P^T and
 // dS^T are A operands in tensor memory (over S^T and dP^T, as packed bf16).
 // dV += P^T dO and the next S^T run while the warps form dS^T; dK += dS^T Q and
 // the next dP^T run under the next exponentials.
-// In both, eight warps work on a tile: two per quarter of its rows, 64 columns
-// each, whose packed result goes to the first 32 of their own columns.
+// In both, sixteen warps work on a tile: four per quarter of its rows, 32 columns
+// each, whose packed result goes to the first 16 of their own columns.
 #include "xattn.cuh"
 
 namespace nvfp4 {
 namespace xattn {
 
-constexpr int kBwdThreads = 384;
-constexpr int kBwdRegsLow = 64;               // 128 x 64 + 256 x 208 <= 384 x 168
-constexpr int kBwdRegsHigh = 208;
-static_assert(128 * kBwdRegsLow + 256 * kBwdRegsHigh <= kBwdThreads * 168, "register split exceeds the launch budget");
+constexpr int kBwdThreads = 640;
+constexpr int kBwdWarps = 16;                 // on a tile
+constexpr int kBwdCols = 32;                  // columns of one
+constexpr int kBwdRegsLow = 64;               // 128 x 64 + 512 x 104 <= 640 x 96
+constexpr int kBwdRegsHigh = 104;
+static_assert(128 * kBwdRegsLow + 512 * kBwdRegsHigh <= kBwdThreads * 96, "register split exceeds the launch budget");
 
 // A ring of shared-memory tiles; `count` loads so far.
 struct TileRing {
@@ -57,8 +60,8 @@ struct TileRing {
     }
 };
 
-// A operand in TMEM, step kk: packed values of columns [0, 64) at `base`, of [64, 128) 64 columns on.
-__device__ __forceinline__ uint32_t packed_a(uint32_t base, int kk) { return base + (kk >> 2) * 64 + (kk & 3) * 8; }
+// The packed values of 32 columns start where those columns did: an A operand of two steps a group.
+constexpr int kPackedGroup = kBwdCols / 16;
 
 // ------------------------------------------------------------------ D
 constexpr int kDeltaThreads = 256;
@@ -103,7 +106,7 @@ __global__ void __launch_bounds__(kDeltaThreads) delta_kernel(const nvfp4_heads 
 
 // ------------------------------------------------------------------ dQ
 struct DqParams {
-    MapAxes aq, ag, ak, av;
+    MapAxes aq, ag, ak, av, ad;
     nvfp4_heads dq;
     const float* lse;
     const float* delta;
@@ -147,8 +150,6 @@ struct DqWalk {
         it = dq_next(p, blockIdx.x, item);
     }
     __device__ bool valid(const DqParams& p) const { return it < p.items; }
-    __device__ int keys_here() const { return min(item.keys - j * kRows, kRows); }
-    __device__ bool last() const { return j == item.steps - 1; }
     __device__ void next(const DqParams& p) {
         if (++j == item.steps) {
             j = 0;
@@ -162,14 +163,15 @@ constexpr uint32_t kDqS = 0, kDqP = 256, kDqO = 384;      // S: [128 (s & 1), + 
 
 __global__ void __launch_bounds__(kBwdThreads, 1)
 xattn_dq_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_g,
-                const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v, const DqParams p) {
+                const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
+                const __grid_constant__ CUtensorMap tmap_dq, const DqParams p) {
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t q_full[kMaxQ], q_empty[kMaxQ], k_full[kMaxK], k_empty[kMaxK], v_full[kMaxV], v_empty[kMaxV];
     __shared__ __align__(8) uint64_t s_full[2], dp_full, ds_ready, dq_full, drain;
-    __shared__ uint32_t tmem_base_sh;
+    __shared__ uint32_t k_info[kMaxK], tmem_base_sh;
     __shared__ int abort_sh;
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int tile_bytes = p.chunks * kChunk;
     uint8_t* k_tiles = smem + p.qbufs * tile_bytes;
@@ -180,7 +182,7 @@ xattn_dq_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
         abort_sh = 0;
         for (int i = 0; i < kMaxQ; ++i) {
             mbar_init(&q_full[i], 1);
-            mbar_init(&q_empty[i], 1);
+            mbar_init(&q_empty[i], 1 + kBwdWarps);      // the tile's last product, the warps
         }
         for (int i = 0; i < kMaxK; ++i) {
             mbar_init(&k_full[i], 1);
@@ -193,7 +195,7 @@ xattn_dq_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
         mbar_init(&s_full[0], 1);
         mbar_init(&s_full[1], 1);
         mbar_init(&dp_full, 1);
-        mbar_init(&ds_ready, 8);                    // the eight warps
+        mbar_init(&ds_ready, kBwdWarps);
         mbar_init(&dq_full, 1);
         mbar_init(&drain, 1);
         fence_barrier_init();
@@ -201,6 +203,7 @@ xattn_dq_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
         tma_prefetch_desc(&tmap_g);
         tma_prefetch_desc(&tmap_k);
         tma_prefetch_desc(&tmap_v);
+        tma_prefetch_desc(&tmap_dq);
     }
     if (warp == 1) {
         tmem_alloc(&tmem_base_sh, 512);
@@ -219,9 +222,10 @@ xattn_dq_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
             DqWalk w;
             bool ok = true;
             auto load = [&](TileRing& ring, uint64_t* full, uint64_t* empty, uint8_t* tiles, const CUtensorMap* map, int h, int l,
-                            int b) {
+                            int b, uint32_t* info, uint32_t value) {
                 if (!warp_wait(&empty[ring.slot], ring.phase ^ 1u, wc)) return false;
-                if (elect_one()) {
+                if (lane == 0) {
+                    if (info) info[ring.slot] = value;
                     mbar_arrive_expect_tx(&full[ring.slot], (uint32_t)tile_bytes);
                     load_tile(tiles + ring.slot * tile_bytes, map, &full[ring.slot], p.chunks, kChunk, h, l, b);
                 }
@@ -232,10 +236,15 @@ xattn_dq_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
             for (w.start(p); ok && w.valid(p); w.next(p)) {
                 const DqItem& i = w.item;
                 const int hk = i.h / p.group;
-                ok = (w.j > 0 || load(rq, q_full, q_empty, smem, &tmap_q, i.h * p.aq.h, i.q0, i.b * p.aq.b)) &&
-                     load(rk, k_full, k_empty, k_tiles, &tmap_k, hk * p.ak.h, w.j * kRows, i.b * p.ak.b) &&
-                     (w.j > 0 || load(rq, q_full, q_empty, smem, &tmap_g, i.h * p.ag.h, i.q0, i.b * p.ag.b)) &&
-                     load(rv, v_full, v_empty, v_tiles, &tmap_v, hk * p.av.h, w.j * kRows, i.b * p.av.b);
+                ok = (w.j > 0 || load(rq, q_full, q_empty, smem, &tmap_q, i.h * p.aq.h, i.q0, i.b * p.aq.b, nullptr, 0)) &&
+                     load(rk, k_full, k_empty, k_tiles, &tmap_k, hk * p.ak.h, w.j * kRows, i.b * p.ak.b, k_info,
+                          step_info(i.keys, p.Lk, w.j, i.steps, false)) &&
+                     (w.j > 0 || load(rq, q_full, q_empty, smem, &tmap_g, i.h * p.ag.h, i.q0, i.b * p.ag.b, nullptr, 0)) &&
+                     load(rv, v_full, v_empty, v_tiles, &tmap_v, hk * p.av.h, w.j * kRows, i.b * p.av.b, nullptr, 0);
+            }
+            if (ok && warp_wait(&k_empty[rk.slot], rk.phase ^ 1u, wc) && lane == 0) {
+                k_info[rk.slot] = 0;
+                mbar_arrive(&k_full[rk.slot]);
             }
             if (!ok && lane == 0) {                 // a block that gave up still waits for its loads in flight
                 int dummy = 0;
@@ -253,40 +262,32 @@ xattn_dq_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
             TileRing ks(p.kbufs), kq(p.kbufs), rv(p.vbufs);      // K as S and as dQ use it, V
             TileRing qs(p.qbufs), qp(p.qbufs);                   // Q tiles (even entries), dO tiles (odd ones)
             qp.next();
-            DqWalk ws, wp, wq;                                   // steps of S, dP, dQ
-            ws.start(p);
-            wp = wq = ws;
-            uint32_t s_at = 0;                                   // S products so far
-            uint32_t done = 0;                                   // dS so far
+            uint32_t s_at = 0, done = 0;                         // S products, dS so far
             int q_slot = 0, g_slot = 0;
             bool ok = true;
 
-            auto issue_s = [&]() {
-                if (ws.j == 0) {
+            // S of the step whose K tile comes next; returns its description
+            auto issue_s = [&]() -> uint32_t {
+                if (!(ok = warp_wait(&k_full[ks.slot], ks.phase, wc))) return 0;
+                const uint32_t info = k_info[ks.slot];
+                if (info == 0) return 0;
+                if (info & kInfoFirst) {
                     q_slot = qs.slot;
-                    if (!warp_wait(&q_full[qs.slot], qs.phase, wc)) return false;
+                    if (!(ok = warp_wait(&q_full[qs.slot], qs.phase, wc))) return 0;
                     qs.next();
                     qs.next();
                 }
-                if (!warp_wait(&k_full[ks.slot], ks.phase, wc)) return false;
                 tc_fence_after();
-                if (elect_one()) {
-                    const uint32_t qt = q_sm + q_slot * tile_bytes, kt = k_sm + ks.slot * tile_bytes;
-                    const uint32_t idesc = idesc_kk((ws.keys_here() + 15) & ~15);
-                    for (int kk = 0; kk < dsteps; ++kk)
-                        tc_mma_bf16(tmem + kDqS + (s_at & 1u) * 128, desc_kmajor(qt, kk, kChunk), desc_kmajor(kt, kk, kChunk),
-                                    idesc, kk != 0 ? 1u : 0u);
-                    tc_commit(&s_full[s_at & 1u]);
-                    if (ws.last()) tc_commit(&q_empty[q_slot]);
-                }
-                __syncwarp();
+                product_kk(tmem + kDqS + (s_at & 1u) * 128, q_sm + q_slot * tile_bytes, k_sm + ks.slot * tile_bytes,
+                           idesc_kk((int)((info & kInfoKeys) + 15) & ~15), dsteps);
+                commit(&s_full[s_at & 1u]);
+                if (info & kInfoLast) commit(&q_empty[q_slot]);
                 ks.next();
                 ++s_at;
-                ws.next(p);
-                return true;
+                return info;
             };
-            auto issue_dp = [&]() {
-                if (wp.j == 0) {
+            auto issue_dp = [&](uint32_t info) {
+                if (info & kInfoFirst) {
                     g_slot = qp.slot;
                     if (!warp_wait(&q_full[qp.slot], qp.phase, wc)) return false;
                     qp.next();
@@ -294,60 +295,34 @@ xattn_dq_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
                 }
                 if (!warp_wait(&v_full[rv.slot], rv.phase, wc)) return false;
                 tc_fence_after();
-                if (elect_one()) {
-                    const uint32_t gt = q_sm + g_slot * tile_bytes, vt = v_sm + rv.slot * tile_bytes;
-                    const uint32_t idesc = idesc_kk((wp.keys_here() + 15) & ~15);
-                    for (int kk = 0; kk < dsteps; ++kk)
-                        tc_mma_bf16(tmem + kDqP, desc_kmajor(gt, kk, kChunk), desc_kmajor(vt, kk, kChunk), idesc,
-                                    kk != 0 ? 1u : 0u);
-                    tc_commit(&dp_full);
-                    tc_commit(&v_empty[rv.slot]);
-                    if (wp.last()) tc_commit(&q_empty[g_slot]);
-                }
-                __syncwarp();
+                product_kk(tmem + kDqP, q_sm + g_slot * tile_bytes, v_sm + rv.slot * tile_bytes,
+                           idesc_kk((int)((info & kInfoKeys) + 15) & ~15), dsteps);
+                commit(&dp_full);
+                commit(&v_empty[rv.slot]);
+                if (info & kInfoLast) commit(&q_empty[g_slot]);
                 rv.next();
-                wp.next(p);
                 return true;
             };
 
-            if (ws.valid(p)) {
-                ok = issue_s() && issue_dp();
-                if (ok && ws.valid(p)) ok = issue_s();
-            }
-            while (ok && wq.valid(p)) {
-                const int n = wq.keys_here();
-                ok = warp_wait(&ds_ready, done & 1u, wc);
-                if (!ok) break;
-                if (wp.valid(p) && !(ok = issue_dp())) break;
-                if ((n & 15) != 0 && wq.item.keys < p.Lk) {
-                    // keys past the sample's length meet dS = 0, but may be NaN: the rest of the last
-                    // 16 rows reads as zeros (rows past the tensor already do; S of the step is done)
-                    uint8_t* row = k_tiles + kq.slot * tile_bytes;
-                    const int rows = 16 - (n & 15);
-                    for (int i = lane; i < rows * 8 * p.chunks; i += 32) {
-                        const int c = i / (rows * 8), r = i - c * rows * 8;
-                        *reinterpret_cast<uint4*>(row + c * kChunk + n * 128 + r * 16) = make_uint4(0, 0, 0, 0);
-                    }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                }
+            uint32_t cur = issue_s(), nxt = 0;
+            if (cur) ok = issue_dp(cur);
+            if (ok && cur) nxt = issue_s();
+            while (ok && cur) {
+                const int n = (int)(cur & kInfoKeys);
+                if (!(ok = warp_wait(&ds_ready, done & 1u, wc))) break;
+                if (nxt && !(ok = issue_dp(nxt))) break;
+                if (cur & kInfoZero) zero_rest(k_tiles + kq.slot * tile_bytes, n, p.chunks, lane);   // S of the step is done
                 tc_fence_after();
-                if (elect_one()) {
-                    const uint32_t kt = k_sm + kq.slot * tile_bytes, a = tmem + kDqS + (done & 1u) * 128;
-                    const int ksteps = (n + 15) >> 4;
-                    for (int kk = 0; kk < ksteps; ++kk)
-                        tc_mma_bf16_ta(tmem + kDqO, packed_a(a, kk), desc_mnmajor(kt, kk, kChunk), idesc_o,
-                                       (wq.j | kk) != 0 ? 1u : 0u);
-                    tc_commit(&k_empty[kq.slot]);
-                    if (wq.last()) tc_commit(&dq_full);
-                }
-                __syncwarp();
+                product_tmem<kPackedGroup>(tmem + kDqO, tmem + kDqS + (done & 1u) * 128, k_sm + kq.slot * tile_bytes,
+                                           idesc_o, (n + 15) >> 4, (cur & kInfoFirst) == 0);
+                commit(&k_empty[kq.slot]);
+                if (cur & kInfoLast) commit(&dq_full);
                 kq.next();
                 ++done;
-                wq.next(p);
-                if (ws.valid(p)) ok = issue_s();
+                cur = nxt;
+                if (nxt) nxt = issue_s();
             }
-            if (elect_one()) tc_commit(&drain);
+            commit(&drain);
             __syncwarp();
             int dummy = 0;
             WaitCtx w2{&dummy, p.dev_status};
@@ -358,106 +333,125 @@ xattn_dq_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
         // ------------------------------------------------------------ dS, and dQ of finished items
         const int g = (warp - 4) >> 2, quarter = warp & 3, r = quarter * 32 + lane;
         const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
-        const uint32_t tbase = tmem + lane_base + g * 64;
+        const uint32_t tbase = tmem + lane_base + g * kBwdCols;
         uint32_t step = 0, outs = 0;
         bool ok = true;
 
         auto row_at = [&](const DqItem& i) {
             return static_cast<uint16_t*>(p.dq.data) + (int64_t)i.b * p.dq.batch_stride + (int64_t)(i.q0 + r) * p.dq.token_stride +
-                   (int64_t)i.h * p.dq.head_stride;
+                   (int64_t)i.h * p.dq.head_stride + g * kBwdCols;
         };
+        const int cols = min(max(p.d - g * kBwdCols, 0), kBwdCols);        // of d this warp reads out
+        // Q and dO tiles of the items in the order of their loads: the warps let go of a Q tile at once,
+        // of a dO tile when dQ has gone out from it
+        int q_slot = 0, g_slot = 1 % p.qbufs, from = -1;
+        uint8_t* const staged = smem + (g * 4 + quarter) * 2048;           // + slot: 32 rows of 64 bytes, 64-byte swizzle
         auto read_out = [&](const DqItem& i) {
             if (!warp_wait(&dq_full, outs & 1u, wc)) return false;
             ++outs;
-            tc_fence_after();
-            uint16_t* dst = row_at(i);
-#pragma unroll
-            for (int c2 = 0; c2 < 2; ++c2) {
-                const int col = g * 64 + c2 * 32;
-                if (col >= p.d) break;
+            if (cols > 0) {
+                tc_fence_after();
                 uint32_t o[32];
-                tmem_ld_32x32b_x32(tbase + kDqO + c2 * 32, o);
+                tmem_ld_32x32b_x32(tbase + kDqO, o);
                 tmem_ld_wait();
-                if (i.q0 + r < p.Lq) {
+                uint8_t* dst = staged + from * tile_bytes;
 #pragma unroll
-                    for (int e = 0; e < 32; e += 8) {
-                        if (col + e >= p.d) break;
-                        uint32_t w[4];
+                for (int e = 0; e < 4; ++e) {
+                    uint32_t w[4];
 #pragma unroll
-                        for (int u = 0; u < 4; ++u)
-                            w[u] = pack_bf16(__uint_as_float(o[e + 2 * u]) * p.scale, __uint_as_float(o[e + 2 * u + 1]) * p.scale);
-                        *reinterpret_cast<uint4*>(dst + col + e) = make_uint4(w[0], w[1], w[2], w[3]);
-                    }
+                    for (int u = 0; u < 4; ++u)
+                        w[u] = pack_bf16(__uint_as_float(o[8 * e + 2 * u]) * p.scale, __uint_as_float(o[8 * e + 2 * u + 1]) * p.scale);
+                    *reinterpret_cast<uint4*>(dst + lane * 64 + ((e ^ ((lane >> 1) & 3)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    if (i.q0 + quarter * 32 < p.Lq)
+                        tma_store_4d(&tmap_dq, dst, g * kBwdCols, i.h * p.ad.h, i.q0 + quarter * 32, i.b * p.ad.b);
+                    bulk_commit_group();
                 }
             }
             return true;
         };
+        auto release = [&]() {                      // the dO tile, once dQ has been read from it
+            if (lane == 0) {
+                bulk_wait_group_read<0>();
+                mbar_arrive(&q_empty[from]);
+            }
+            from = -1;
+            __syncwarp();
+        };
 
-        DqItem prev;
+        // the next item's lse (times log2(e)) and D are on their way while this one's steps run
+        auto fetch = [&](int it, DqItem& i, float& l, float& delta) {
+            i = dq_item(p, it);
+            const int64_t at = ((int64_t)i.b * p.H + i.h) * p.Lq + i.q0 + r;
+            const bool have = i.q0 + r < p.Lq;
+            l = have ? __ldg(p.lse + at) : INFINITY;
+            delta = have ? __ldg(p.delta + at) : 0.0f;
+        };
+        DqItem prev, item, following;
+        float lse = 0.0f, dl = 0.0f, next_lse = 0.0f, next_dl = 0.0f;
         bool pending = false;
-        for (int it = blockIdx.x; ok && it < p.items; it += gridDim.x) {
-            const DqItem item = dq_item(p, it);
-            const bool have = item.q0 + r < p.Lq;
+        if ((int)blockIdx.x < p.items) fetch(blockIdx.x, item, lse, dl);
+        for (int it = blockIdx.x; ok && it < p.items; it += gridDim.x, item = following, lse = next_lse, dl = next_dl) {
+            if (it + (int)gridDim.x < p.items) fetch(it + gridDim.x, following, next_lse, next_dl);
             if (item.steps == 0) {
-                if (have)
-                    for (int i = g * 64; i < min(p.d, g * 64 + 64); i += 8)
-                        *reinterpret_cast<uint4*>(row_at(item) + i) = make_uint4(0, 0, 0, 0);
+                if (item.q0 + r < p.Lq)
+                    for (int i = 0; i < cols; i += 8) *reinterpret_cast<uint4*>(row_at(item) + i) = make_uint4(0, 0, 0, 0);
                 continue;
             }
-            const int64_t at = ((int64_t)item.b * p.H + item.h) * p.Lq + item.q0 + r;
-            const float lse2 = have ? __ldg(p.lse + at) * kLog2e : INFINITY, dl = have ? __ldg(p.delta + at) : 0.0f;
+            const float lse2 = lse * kLog2e;
             for (int j = 0; j < item.steps; ++j, ++step) {
-                const int n = min(max(item.keys - j * kRows - g * 64, 0), 64);      // this warp's keys
+                const int n = min(max(item.keys - j * kRows - g * kBwdCols, 0), kBwdCols);      // this warp's keys
                 const uint32_t ts = tbase + kDqS + (step & 1u) * 128, tp = tbase + kDqP;
                 if (!(ok = warp_wait(&s_full[step & 1u], (step >> 1) & 1u, wc))) break;
                 tc_fence_after();
-                uint32_t v[64];
+                if (j == 0 && lane == 0) mbar_arrive(&q_empty[q_slot]);
+                uint32_t v[32];
+                if (n > 0) {
+                    tmem_ld_32x32b_x32(ts, v);
+                    tmem_ld_wait();
+                }
 #pragma unroll
-                for (int c2 = 0; c2 < 2; ++c2)
-                    if (c2 * 32 < n) tmem_ld_32x32b_x32(ts + c2 * 32, *reinterpret_cast<uint32_t(*)[32]>(&v[c2 * 32]));
-                tmem_ld_wait();
-#pragma unroll
-                for (int i = 0; i < 64; ++i) v[i] = __float_as_uint(ex2(fmaf(__uint_as_float(v[i]), p.c, -lse2)));
+                for (int i = 0; i < 32; i += 2) {
+                    const F2 x = fma2({__uint_as_float(v[i]), __uint_as_float(v[i + 1])}, {p.c, p.c}, {-lse2, -lse2});
+                    v[i] = __float_as_uint(ex2(x.x));
+                    v[i + 1] = __float_as_uint(ex2(x.y));
+                }
                 if (pending) {
                     if (!(ok = read_out(prev))) break;
                     pending = false;
                 }
                 if (!(ok = warp_wait(&dp_full, step & 1u, wc))) break;
                 tc_fence_after();
-                uint32_t w[32];
-#pragma unroll
-                for (int c2 = 0; c2 < 2; ++c2) {
-                    if (c2 * 32 >= n) {
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) w[c2 * 16 + i] = 0;
-                        continue;
-                    }
-                    uint32_t dp[32];
-                    tmem_ld_32x32b_x32(tp + c2 * 32, dp);
+                if (n > 0) {
+                    uint32_t dp[32], w[16];
+                    tmem_ld_32x32b_x32(tp, dp);
                     tmem_ld_wait();
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        dp[i] = __float_as_uint((__uint_as_float(dp[i]) - dl) * __uint_as_float(v[c2 * 32 + i]));
-                    if (n < 64) {
+                    for (int i = 0; i < 32; i += 2) {
+                        const F2 x = mul2(add2({__uint_as_float(dp[i]), __uint_as_float(dp[i + 1])}, {-dl, -dl}),
+                                          {__uint_as_float(v[i]), __uint_as_float(v[i + 1])});
                         // keys past the length: zero, whatever was computed there
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (c2 * 32 + i >= n) dp[i] = 0;
+                        w[i / 2] = pack_bf16(i < n ? x.x : 0.0f, i + 1 < n ? x.y : 0.0f);
                     }
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        w[c2 * 16 + i] = pack_bf16(__uint_as_float(dp[2 * i]), __uint_as_float(dp[2 * i + 1]));
+                    tmem_st_x16(ts, w);
                 }
-                if (n > 0) tmem_st_x32(ts, w);
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&ds_ready);
+                if (from >= 0 && !pending) release();
             }
             prev = item;
             pending = ok;
+            from = g_slot;
+            q_slot = (q_slot + 2) % p.qbufs;
+            g_slot = (g_slot + 2) % p.qbufs;
         }
-        if (ok && pending) read_out(prev);
+        if (ok && pending && read_out(prev)) release();
+        if (lane == 0) bulk_wait_group_read<0>();
     }
 
     tc_fence_before();
@@ -501,7 +495,7 @@ xattn_dkv_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
     const int bh = unit / p.ktiles, k0 = (unit - bh * p.ktiles) * kRows;
     const int b = bh / p.Hkv, hk = bh - b * p.Hkv;
     const int keys = keys_of(p.kv_lens, b, p.Lk);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     if (k0 >= keys) {
         // no valid key: zeros where no later kernel writes them
         if (!p.partial)
@@ -531,11 +525,11 @@ xattn_dkv_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
         mbar_init(&v_full, 1);
         mbar_init(&s_full, 1);
         mbar_init(&dp_full, 1);
-        mbar_init(&p_ready, 8);                     // the eight warps
-        mbar_init(&ds_ready, 8);
+        mbar_init(&p_ready, kBwdWarps);
+        mbar_init(&ds_ready, kBwdWarps);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&st_full[i], 32);
-            mbar_init(&st_empty[i], 8);
+            mbar_init(&st_empty[i], kBwdWarps);
         }
         mbar_init(&drain, 1);
         fence_barrier_init();
@@ -604,57 +598,48 @@ xattn_dkv_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
             TileRing rs(p.qbufs), rp(p.qbufs), rv(p.qbufs), rk(p.qbufs);    // Q for S, dO for dP, dO for dV, Q for dK
             rp.next();
             rv.next();
-            auto queries = [&](int t) { return min(p.Lq - (t % p.qtiles) * kRows, kRows); };
-            // S^T or dP^T of step t: rows = keys, columns = queries
-            auto scores = [&](int t, TileRing& ring, uint32_t a_sm, uint32_t col, uint64_t* bar) {
+            // S^T or dP^T of a step with n queries: rows = keys, columns = queries
+            auto scores = [&](int n, TileRing& ring, uint32_t a_sm, uint32_t col, uint64_t* bar) {
                 if (!warp_wait(&qg_full[ring.slot], ring.phase, wc)) return false;
                 tc_fence_after();
-                if (elect_one()) {
-                    const uint32_t bt = qg_sm + ring.slot * tile_bytes;
-                    const uint32_t idesc = idesc_kk((queries(t) + 15) & ~15);
-                    for (int kk = 0; kk < dsteps; ++kk)
-                        tc_mma_bf16(tmem + col, desc_kmajor(a_sm, kk, kChunk), desc_kmajor(bt, kk, kChunk), idesc,
-                                    kk != 0 ? 1u : 0u);
-                    tc_commit(bar);
-                }
-                __syncwarp();
+                product_kk(tmem + col, a_sm, qg_sm + ring.slot * tile_bytes, idesc_kk((n + 15) & ~15), dsteps);
+                commit(bar);
                 ring.next();
                 ring.next();
                 return true;
             };
             // dV or dK += (P^T or dS^T) (dO or Q)
-            auto update = [&](int t, TileRing& ring, uint32_t a, uint32_t col) {
+            auto update = [&](int n, TileRing& ring, uint32_t a, uint32_t col, bool accumulate) {
                 tc_fence_after();
-                if (elect_one()) {
-                    const uint32_t bt = qg_sm + ring.slot * tile_bytes;
-                    const int ksteps = (queries(t) + 15) >> 4;
-                    for (int kk = 0; kk < ksteps; ++kk)
-                        tc_mma_bf16_ta(tmem + col, packed_a(tmem + a, kk), desc_mnmajor(bt, kk, kChunk), idesc_o,
-                                       t > first || kk != 0 ? 1u : 0u);
-                    tc_commit(&qg_empty[ring.slot]);
-                }
-                __syncwarp();
+                product_tmem<kPackedGroup>(tmem + col, tmem + a, qg_sm + ring.slot * tile_bytes, idesc_o, (n + 15) >> 4,
+                                           accumulate);
+                commit(&qg_empty[ring.slot]);
                 ring.next();
                 ring.next();
             };
-            bool ok = warp_wait(&k_full, 0, wc) && scores(first, rs, k_sm, kKvS, &s_full) && warp_wait(&v_full, 0, wc) &&
-                      scores(first, rp, v_sm, kKvP, &dp_full);
-            for (int t = first; ok && t < last; ++t) {
-                const uint32_t ph = (uint32_t)(t - first) & 1u;
+            int q0 = (first % p.qtiles) * kRows;                 // first query of the step
+            int n = min(p.Lq - q0, kRows);
+            bool ok = warp_wait(&k_full, 0, wc) && scores(n, rs, k_sm, kKvS, &s_full) && warp_wait(&v_full, 0, wc) &&
+                      scores(n, rp, v_sm, kKvP, &dp_full);
+            uint32_t ph = 0;
+            for (int t = first; ok && t < last; ++t, ph ^= 1u) {
+                q0 = q0 + kRows < p.Lq ? q0 + kRows : 0;
+                const int n2 = min(p.Lq - q0, kRows);            // of the next step
                 if (!(ok = warp_wait(&p_ready, ph, wc))) break;
-                update(t, rv, kKvS, kKvV);
-                if (t + 1 < last && !(ok = scores(t + 1, rs, k_sm, kKvS, &s_full))) break;
+                update(n, rv, kKvS, kKvV, t > first);
+                if (t + 1 < last && !(ok = scores(n2, rs, k_sm, kKvS, &s_full))) break;
                 if (!(ok = warp_wait(&ds_ready, ph, wc))) break;
-                update(t, rk, kKvP, kKvK);
-                if (t + 1 < last) ok = scores(t + 1, rp, v_sm, kKvP, &dp_full);
+                update(n, rk, kKvP, kKvK, t > first);
+                if (t + 1 < last) ok = scores(n2, rp, v_sm, kKvP, &dp_full);
+                n = n2;
             }
-            if (elect_one()) tc_commit(&drain);
+            commit(&drain);
             __syncwarp();
             int dummy = 0;
             WaitCtx w2{&dummy, p.dev_status};
             mbar_wait(&drain, 0, w2);
         } else if (warp == 2) {
-            // -------------------------------------------------------- lse (times log2(e)) and D of the steps' queries
+            // -------------------------------------------------------- -lse (times log2(e)) and -D of the steps' queries
             bool ok = true;
             for (int t = first; ok && t < last; ++t) {
                 const int s = (t - first) & 1;
@@ -665,8 +650,8 @@ xattn_dkv_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const bool have = q0 + lane + 32 * i < p.Lq;
-                    l[i] = have ? __ldg(p.lse + at + lane + 32 * i) * kLog2e : INFINITY;
-                    dl[i] = have ? __ldg(p.delta + at + lane + 32 * i) : 0.0f;
+                    l[i] = have ? -(__ldg(p.lse + at + lane + 32 * i) * kLog2e) : -INFINITY;
+                    dl[i] = have ? -__ldg(p.delta + at + lane + 32 * i) : 0.0f;
                 }
                 if (!(ok = warp_wait(&st_empty[s], (((uint32_t)(t - first) >> 1) & 1u) ^ 1u, wc))) break;
 #pragma unroll
@@ -682,41 +667,38 @@ xattn_dkv_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
         // ------------------------------------------------------------ P^T and dS^T, a key per thread
         const int g = (warp - 4) >> 2, quarter = warp & 3, r = quarter * 32 + lane;
         const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
-        const uint32_t ts = tmem + lane_base + kKvS + g * 64, tp = tmem + lane_base + kKvP + g * 64;
+        const uint32_t ts = tmem + lane_base + kKvS + g * kBwdCols, tp = tmem + lane_base + kKvP + g * kBwdCols;
         bool ok = true;
         for (int t = first; t < last; ++t) {
             const int s = (t - first) & 1;
             const uint32_t ph = (uint32_t)(t - first) & 1u;
-            const float4* lse4 = reinterpret_cast<const float4*>(&st_lse[s][g * 64]);
-            const float4* del4 = reinterpret_cast<const float4*>(&st_delta[s][g * 64]);
+            const float4* lse4 = reinterpret_cast<const float4*>(&st_lse[s][g * kBwdCols]);
+            const float4* del4 = reinterpret_cast<const float4*>(&st_delta[s][g * kBwdCols]);
             if (!(ok = warp_wait(&st_full[s], ((uint32_t)(t - first) >> 1) & 1u, wc) && warp_wait(&s_full, ph, wc))) break;
             tc_fence_after();
-            uint32_t v[64], w[16];
-            tmem_ld_32x32b_x32(ts, *reinterpret_cast<uint32_t(*)[32]>(&v[0]));
-            tmem_ld_32x32b_x32(ts + 32, *reinterpret_cast<uint32_t(*)[32]>(&v[32]));
+            uint32_t v[32], w[16];
+            tmem_ld_32x32b_x32(ts, v);
             tmem_ld_wait();
             // columns past the last query hold anything: -lse = -infinity alone would leave NaN there
-            const int nq = p.Lq - (t % p.qtiles) * kRows - g * 64;
-            if (nq < 64) {
+            const int nq = p.Lq - (t % p.qtiles) * kRows - g * kBwdCols;
+            if (nq < kBwdCols) {
 #pragma unroll
-                for (int i = 0; i < 64; ++i)
+                for (int i = 0; i < 32; ++i)
                     if (i >= nq) v[i] = 0;
             }
 #pragma unroll
-            for (int c2 = 0; c2 < 2; ++c2) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float4 l = lse4[c2 * 8 + i];
-                    uint32_t* e = v + c2 * 32 + 4 * i;
-                    e[0] = __float_as_uint(ex2(fmaf(__uint_as_float(e[0]), p.c, -l.x)));
-                    e[1] = __float_as_uint(ex2(fmaf(__uint_as_float(e[1]), p.c, -l.y)));
-                    e[2] = __float_as_uint(ex2(fmaf(__uint_as_float(e[2]), p.c, -l.z)));
-                    e[3] = __float_as_uint(ex2(fmaf(__uint_as_float(e[3]), p.c, -l.w)));
-                    w[2 * i] = pack_bf16(__uint_as_float(e[0]), __uint_as_float(e[1]));
-                    w[2 * i + 1] = pack_bf16(__uint_as_float(e[2]), __uint_as_float(e[3]));
-                }
-                tmem_st_x16(ts + c2 * 16, w);
+            for (int i = 0; i < 8; ++i) {
+                const float4 l = lse4[i];                            // kept negated
+                const F2 x = fma2({__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1])}, {p.c, p.c}, {l.x, l.y});
+                const F2 y = fma2({__uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3])}, {p.c, p.c}, {l.z, l.w});
+                v[4 * i] = __float_as_uint(ex2(x.x));
+                v[4 * i + 1] = __float_as_uint(ex2(x.y));
+                v[4 * i + 2] = __float_as_uint(ex2(y.x));
+                v[4 * i + 3] = __float_as_uint(ex2(y.y));
+                w[2 * i] = pack_bf16(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]));
+                w[2 * i + 1] = pack_bf16(__uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3]));
             }
+            tmem_st_x16(ts, w);
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
@@ -724,30 +706,25 @@ xattn_dkv_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
 
             if (!(ok = warp_wait(&dp_full, ph, wc))) break;
             tc_fence_after();
+            uint32_t dp[32];
+            tmem_ld_32x32b_x32(tp, dp);
+            tmem_ld_wait();
+            if (nq < kBwdCols) {
 #pragma unroll
-            for (int c2 = 0; c2 < 2; ++c2) {
-                uint32_t dp[32];
-                tmem_ld_32x32b_x32(tp + c2 * 32, dp);
-                tmem_ld_wait();
-                if (nq < 64) {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        if (c2 * 32 + i >= nq) dp[i] = 0;
-                }
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float4 dl = del4[c2 * 8 + i];
-                    const int at = c2 * 32 + 4 * i;
-                    const float a0 = (__uint_as_float(dp[4 * i]) - dl.x) * __uint_as_float(v[at]);
-                    const float a1 = (__uint_as_float(dp[4 * i + 1]) - dl.y) * __uint_as_float(v[at + 1]);
-                    const float a2 = (__uint_as_float(dp[4 * i + 2]) - dl.z) * __uint_as_float(v[at + 2]);
-                    const float a3 = (__uint_as_float(dp[4 * i + 3]) - dl.w) * __uint_as_float(v[at + 3]);
-                    w[2 * i] = pack_bf16(a0, a1);
-                    w[2 * i + 1] = pack_bf16(a2, a3);
-                }
-                // over this warp's own columns, which it has read so far
-                tmem_st_x16(tp + c2 * 16, w);
+                for (int i = 0; i < 32; ++i)
+                    if (i >= nq) dp[i] = 0;
             }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float4 dl = del4[i];                           // kept negated
+                const F2 x = mul2(add2({__uint_as_float(dp[4 * i]), __uint_as_float(dp[4 * i + 1])}, {dl.x, dl.y}),
+                                  {__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1])});
+                const F2 y = mul2(add2({__uint_as_float(dp[4 * i + 2]), __uint_as_float(dp[4 * i + 3])}, {dl.z, dl.w}),
+                                  {__uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3])});
+                w[2 * i] = pack_bf16(x.x, x.y);
+                w[2 * i + 1] = pack_bf16(y.x, y.y);
+            }
+            tmem_st_x16(tp, w);
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
@@ -756,42 +733,37 @@ xattn_dkv_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
                 mbar_arrive(&ds_ready);
             }
         }
-        // the sums: this thread's key, 64 of the d columns
-        if (ok && warp_wait(&drain, 0, wc)) {
+        // the sums: this thread's key, 32 of the d columns
+        const int cols = min(max(p.d - g * kBwdCols, 0), kBwdCols);
+        if (ok && warp_wait(&drain, 0, wc) && cols > 0) {
             tc_fence_after();
 #pragma unroll 1
             for (int o = 0; o < 2; ++o) {
                 const float f = o == 0 ? p.scale : 1.0f;
                 const nvfp4_heads& t = o == 0 ? p.dk : p.dv;
-                const uint32_t from = tmem + lane_base + (o == 0 ? kKvK : kKvV) + g * 64;
-                uint16_t* dst = static_cast<uint16_t*>(t.data) + (int64_t)b * t.batch_stride + (int64_t)(k0 + r) * t.token_stride +
-                                (int64_t)hk * t.head_stride;
-                float* part = p.partial + (((int64_t)split * (gridDim.x / p.splits) + unit) * 2 + o) * p.d * kRows;
+                uint32_t x[32];
+                tmem_ld_32x32b_x32(tmem + lane_base + (o == 0 ? kKvK : kKvV) + g * kBwdCols, x);
+                tmem_ld_wait();
+                if (p.partial) {
+                    float* part = p.partial + (((int64_t)split * (gridDim.x / p.splits) + unit) * 2 + o) * p.d * kRows +
+                                  ((int64_t)g * (kBwdCols / 4) * kRows + r) * 4;
 #pragma unroll
-                for (int c2 = 0; c2 < 2; ++c2) {
-                    const int col = g * 64 + c2 * 32;
-                    if (col >= p.d) break;
-                    uint32_t x[32];
-                    tmem_ld_32x32b_x32(from + c2 * 32, x);
-                    tmem_ld_wait();
-                    if (p.partial) {
+                    for (int e = 0; e < 32; e += 4) {
+                        if (e >= cols) break;
+                        *reinterpret_cast<uint4*>(part + e * kRows) = make_uint4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+                    }
+                } else if (k0 + r < p.Lk) {
+                    const bool valid = k0 + r < keys;
+                    uint16_t* dst = static_cast<uint16_t*>(t.data) + (int64_t)b * t.batch_stride +
+                                    (int64_t)(k0 + r) * t.token_stride + (int64_t)hk * t.head_stride + g * kBwdCols;
 #pragma unroll
-                        for (int e = 0; e < 32; e += 4) {
-                            if (col + e >= p.d) break;
-                            *reinterpret_cast<uint4*>(part + ((int64_t)((col + e) >> 2) * kRows + r) * 4) =
-                                make_uint4(x[e], x[e + 1], x[e + 2], x[e + 3]);
-                        }
-                    } else if (k0 + r < p.Lk) {
-                        const bool valid = k0 + r < keys;
+                    for (int e = 0; e < 32; e += 8) {
+                        if (e >= cols) break;
+                        uint32_t y[4];
 #pragma unroll
-                        for (int e = 0; e < 32; e += 8) {
-                            if (col + e >= p.d) break;
-                            uint32_t y[4];
-#pragma unroll
-                            for (int u = 0; u < 4; ++u)
-                                y[u] = valid ? pack_bf16(__uint_as_float(x[e + 2 * u]) * f, __uint_as_float(x[e + 2 * u + 1]) * f) : 0u;
-                            *reinterpret_cast<uint4*>(dst + col + e) = make_uint4(y[0], y[1], y[2], y[3]);
-                        }
+                        for (int u = 0; u < 4; ++u)
+                            y[u] = valid ? pack_bf16(__uint_as_float(x[e + 2 * u]) * f, __uint_as_float(x[e + 2 * u + 1]) * f) : 0u;
+                        *reinterpret_cast<uint4*>(dst + e) = make_uint4(y[0], y[1], y[2], y[3]);
                     }
                 }
             }
@@ -895,11 +867,12 @@ cudaError_t launch_cross_attention_backward(const CrossAttnArgs& a, int num_sms,
     float* partial = plan.splits > 1 ? reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + plan.delta_bytes) : nullptr;
     const int qtiles = (a.Lq + kRows - 1) / kRows, ktiles = (a.Lk + kRows - 1) / kRows;
     const int chunks = (a.d + 63) / 64, tile_bytes = chunks * kChunk;
-    CUtensorMap mq{}, mg{}, mk{}, mv{};
-    MapAxes aq{}, ag{}, ak{}, av{};
+    CUtensorMap mq{}, mg{}, mk{}, mv{}, md{};
+    MapAxes aq{}, ag{}, ak{}, av{}, ad{};
     if (a.Lq > 0 && a.Lk > 0 &&
         (!make_heads_map(&mq, a.q, a.B, a.Lq, a.H, a.d, kRows, &aq) || !make_heads_map(&mg, a.grad_out, a.B, a.Lq, a.H, a.d, kRows, &ag) ||
-         !make_heads_map(&mk, a.k, a.B, a.Lk, a.Hkv, a.d, kRows, &ak) || !make_heads_map(&mv, a.v, a.B, a.Lk, a.Hkv, a.d, kRows, &av)))
+         !make_heads_map(&mk, a.k, a.B, a.Lk, a.Hkv, a.d, kRows, &ak) || !make_heads_map(&mv, a.v, a.B, a.Lk, a.Hkv, a.d, kRows, &av) ||
+         !make_heads_map(&md, a.dq, a.B, a.Lq, a.H, a.d, 32, &ad, kBwdCols)))
         return cudaErrorInvalidValue;
     cudaError_t e;
     int launches = 0;
@@ -908,12 +881,12 @@ cudaError_t launch_cross_attention_backward(const CrossAttnArgs& a, int num_sms,
         const int64_t per = kDeltaThreads / 16 * kDeltaRows;
         delta_kernel<<<(unsigned)((rows + per - 1) / per), kDeltaThreads, 0, stream>>>(a.grad_out, a.out, delta, rows, a.Lq, a.H, a.d);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
-        DqParams p{aq, ag, ak, av, a.dq, a.lse, delta, a.kv_lens, a.scale * kLog2e, a.scale, a.H, a.Hkv, a.Lq, a.Lk, a.d,
+        DqParams p{aq, ag, ak, av, ad, a.dq, a.lse, delta, a.kv_lens, a.scale * kLog2e, a.scale, a.H, a.Hkv, a.Lq, a.Lk, a.d,
                    a.H / a.Hkv, qtiles, a.B * a.H * qtiles, chunks, chunks == 1 ? 4 : 3, chunks == 1 ? 4 : 3, chunks == 1 ? 4 : 1,
                    a.dev_status};
         const int smem = (p.qbufs + p.kbufs + p.vbufs) * tile_bytes + 1024;
         if ((e = prepare_kernel(reinterpret_cast<const void*>(xattn_dq_kernel), smem)) != cudaSuccess) return e;
-        xattn_dq_kernel<<<p.items < num_sms ? p.items : num_sms, kBwdThreads, smem, stream>>>(mq, mg, mk, mv, p);
+        xattn_dq_kernel<<<p.items < num_sms ? p.items : num_sms, kBwdThreads, smem, stream>>>(mq, mg, mk, mv, md, p);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
         launches += 2;
     }

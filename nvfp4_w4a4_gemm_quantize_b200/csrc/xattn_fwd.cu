@@ -18,8 +18,11 @@
 // tensor core works for one tile while the other's softmax runs, and S of the
 // next tile needs no barrier of its own, since the tensor core takes it after
 // the product that read P.  The order runs on across work items.
-// Warps: 0 loads (three rotating Q tiles, a ring of K and V tiles), 1 issues
+// Warps: 0 loads (four rotating Q tiles, a ring of K and V tiles), 1 issues
 // and owns TMEM, 4-7 and 8-11 softmax and output of A and B, a thread per row.
+// The output goes out by TMA from the item's own Q tile: written from the
+// registers, a row per thread, it took 6400 cycles an item (a 128-byte line per
+// lane and store), as long as two steps.
 // Bound by the exponentials and the tensor core about equally at d = 128 (a
 // pair of 128 x 128 tiles costs 2048 cycles of either), by the exponentials below.
 #include "xattn.cuh"
@@ -28,9 +31,9 @@ namespace nvfp4 {
 namespace xattn {
 
 constexpr int kThreads = 384;
-constexpr int kQBufs = 3;
+constexpr int kQBufs = 4;
 constexpr int kMaxRing = 12;
-constexpr int kRegsLow = 64;                  // 128 x 64 + 256 x 208 <= 384 x 168
+constexpr int kRegsLow = 88;                  // 128 x 88 + 256 x 208 <= 384 x 168
 constexpr int kRegsHigh = 208;
 static_assert(128 * kRegsLow + 256 * kRegsHigh <= kThreads * 168, "register split exceeds the launch budget");
 
@@ -38,7 +41,7 @@ constexpr uint32_t kColS = 0;                 // S_g (and P_g): [128 g, 128 g + 
 constexpr uint32_t kColO = 256;               // O_g: [256 + 128 g, 384 + 128 g)
 
 struct FwdParams {
-    MapAxes aq, ak, av;
+    MapAxes aq, ak, av, ao;
     nvfp4_heads out;
     float* lse;
     const int32_t* kv_lens;
@@ -98,14 +101,14 @@ struct RingAt {
 
 __global__ void __launch_bounds__(kThreads, 1)
 xattn_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
-                 const __grid_constant__ CUtensorMap tmap_v, const FwdParams p) {
+                 const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ CUtensorMap tmap_o, const FwdParams p) {
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t q_full[kQBufs], q_empty[kQBufs], kv_full[kMaxRing], kv_empty[kMaxRing];
     __shared__ __align__(8) uint64_t s_full[2], p_full[2], o_full[2], o_free[2], drain;
-    __shared__ uint32_t tmem_base_sh;
+    __shared__ uint32_t kv_info[kMaxRing], tmem_base_sh;
     __shared__ int abort_sh;
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int tile_bytes = p.chunks * kChunk;
     uint8_t* ring = smem + kQBufs * tile_bytes;
@@ -115,7 +118,7 @@ xattn_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
         abort_sh = 0;
         for (int i = 0; i < kQBufs; ++i) {
             mbar_init(&q_full[i], 1);
-            mbar_init(&q_empty[i], 1);              // the tile's last S product
+            mbar_init(&q_empty[i], 5);              // the tile's last S product, the group's warps
         }
         for (int i = 0; i < kMaxRing; ++i) {
             mbar_init(&kv_full[i], 1);
@@ -132,6 +135,7 @@ xattn_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
         tma_prefetch_desc(&tmap_q);
         tma_prefetch_desc(&tmap_k);
         tma_prefetch_desc(&tmap_v);
+        tma_prefetch_desc(&tmap_o);
     }
     if (warp == 1) {
         tmem_alloc(&tmem_base_sh, 512);
@@ -164,7 +168,8 @@ xattn_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
             };
             auto load_kv = [&](const CUtensorMap* map, const MapAxes& axes, int j) {
                 if (!warp_wait(&kv_empty[at.slot], at.phase ^ 1u, wc)) return false;
-                if (elect_one()) {
+                if (lane == 0) {
+                    kv_info[at.slot] = step_info(item.keys, p.Lk, j, item.steps, item.two);
                     mbar_arrive_expect_tx(&kv_full[at.slot], (uint32_t)tile_bytes);
                     load_tile(ring + at.slot * tile_bytes, map, &kv_full[at.slot], p.chunks, kChunk, item.hk * axes.h,
                               j * kRows, item.b * axes.b);
@@ -177,6 +182,11 @@ xattn_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
                 ok = load_q(0) && load_kv(&tmap_k, p.ak, 0) && (!item.two || load_q(1)) && load_kv(&tmap_v, p.av, 0);
                 for (int j = 1; ok && j < item.steps; ++j) ok = load_kv(&tmap_k, p.ak, j) && load_kv(&tmap_v, p.av, j);
             }
+            if (ok && warp_wait(&kv_empty[at.slot], at.phase ^ 1u, wc) && lane == 0) {
+                kv_info[at.slot] = 0;                            // no more steps
+                mbar_arrive(&kv_full[at.slot]);
+            }
+            __syncwarp();
             // a block that gave up still waits for its loads in flight
             if (!ok && lane == 0) {
                 int dummy = 0;
@@ -195,87 +205,66 @@ xattn_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
             const int dsteps = (p.d + 15) >> 4;
             const uint32_t idesc_o = idesc_kmn(dsteps * 16);
             RingAt kat{0, 0}, vat{1, 0};            // K and V tiles alternate in the ring
-            int q_use = 0;                          // running number of Q tiles
+            RingAt qat{0, 0};
             uint32_t uses[2] = {0, 0}, outs[2] = {0, 0};   // tiles and items of each group so far
-            Item cur, nxt;
             int q_buf[2] = {0, 0};
             bool ok = true;
 
-            // S_g of step j of item `i`; the first product on a K tile waits for it, the last frees it
-            auto issue_s = [&](const Item& i, int j, int g) {
-                if (j == 0) {
-                    q_buf[g] = q_use % kQBufs;
-                    if (!warp_wait(&q_full[q_buf[g]], (uint32_t)(q_use / kQBufs) & 1u, wc)) return false;
-                    ++q_use;
+            // the description of the step whose K tile comes next
+            auto describe = [&]() -> uint32_t {
+                if (!(ok = warp_wait(&kv_full[kat.slot], kat.phase, wc))) return 0;
+                return kv_info[kat.slot];
+            };
+            // S_g of that step; the last product on the K tile frees it
+            auto issue_s = [&](uint32_t info, int g) {
+                if (info & kInfoFirst) {
+                    q_buf[g] = qat.slot;
+                    if (!warp_wait(&q_full[qat.slot], qat.phase, wc)) return false;
+                    qat.advance(1, kQBufs);
                 }
-                if (g == 0 && !warp_wait(&kv_full[kat.slot], kat.phase, wc)) return false;
                 tc_fence_after();
-                if (elect_one()) {
-                    const uint32_t qt = q_sm + q_buf[g] * tile_bytes, kt = ring_sm + kat.slot * tile_bytes;
-                    const int n = min(i.keys - j * kRows, kRows);
-                    const uint32_t idesc = idesc_kk((n + 15) & ~15);
-                    for (int kk = 0; kk < dsteps; ++kk)
-                        tc_mma_bf16(tmem + kColS + g * 128, desc_kmajor(qt, kk, kChunk), desc_kmajor(kt, kk, kChunk), idesc,
-                                    kk != 0 ? 1u : 0u);
-                    tc_commit(&s_full[g]);
-                    if (g == 1 || !i.two) tc_commit(&kv_empty[kat.slot]);
-                    if (j == i.steps - 1) tc_commit(&q_empty[q_buf[g]]);
+                product_kk(tmem + kColS + g * 128, q_sm + q_buf[g] * tile_bytes, ring_sm + kat.slot * tile_bytes,
+                           idesc_kk((int)((info & kInfoKeys) + 15) & ~15), dsteps);
+                commit(&s_full[g]);
+                if (info & kInfoLast) commit(&q_empty[q_buf[g]]);
+                if (g == 1 || !(info & kInfoTwo)) {
+                    commit(&kv_empty[kat.slot]);
+                    kat.advance(2, p.ring);
                 }
-                __syncwarp();
-                if (g == 1 || !i.two) kat.advance(2, p.ring);
                 return true;
             };
 
-            int it = next_item(p, blockIdx.x, cur);
-            if (it < p.items) ok = issue_s(cur, 0, 0) && (!cur.two || issue_s(cur, 0, 1));
-            while (ok && it < p.items) {
-                const int it2 = next_item(p, it + gridDim.x, nxt);
-                for (int j = 0; ok && j < cur.steps; ++j) {
-                    const bool last = j == cur.steps - 1;
-                    const bool more = !last || it2 < p.items;
-                    const Item& ni = last ? nxt : cur;          // the step whose S comes next
-                    const int nj = last ? 0 : j + 1;
-                    const int n = min(cur.keys - j * kRows, kRows);
-                    for (int g = 0; ok && g < (cur.two ? 2 : 1); ++g) {
-                        ok = warp_wait(&p_full[g], uses[g] & 1u, wc) &&
-                             (g == 1 || warp_wait(&kv_full[vat.slot], vat.phase, wc)) &&
-                             // the item's first product overwrites O_g: the previous one's has been read out
-                             (j > 0 || outs[g] == 0 || warp_wait(&o_free[g], (outs[g] - 1) & 1u, wc));
-                        if (!ok) break;
-                        ++uses[g];
-                        const uint32_t vt = ring_sm + vat.slot * tile_bytes;
-                        if (g == 0 && (n & 15) != 0 && cur.keys < p.Lk) {
-                            // values past the sample's length meet P = 0, but may be NaN: the rest
-                            // of the last 16 rows reads as zeros (rows past the tensor already do)
-                            uint8_t* vrow = ring + vat.slot * tile_bytes;
-                            const int rows = 16 - (n & 15);
-                            for (int i = lane; i < rows * 8 * p.chunks; i += 32) {
-                                const int c = i / (rows * 8), r = i - c * rows * 8;
-                                *reinterpret_cast<uint4*>(vrow + c * kChunk + n * 128 + r * 16) = make_uint4(0, 0, 0, 0);
-                            }
-                            fence_proxy_async_smem();
-                            __syncwarp();
-                        }
-                        tc_fence_after();
-                        if (elect_one()) {
-                            const int ksteps = (n + 15) >> 4;
-                            for (int kk = 0; kk < ksteps; ++kk)
-                                tc_mma_bf16_ta(tmem + kColO + g * 128, tmem + kColS + g * 128 + kk * 8,
-                                               desc_mnmajor(vt, kk, kChunk), idesc_o, (j | kk) != 0 ? 1u : 0u);
-                            if (g == 1 || !cur.two) tc_commit(&kv_empty[vat.slot]);
-                            if (last) tc_commit(&o_full[g]);
-                        }
-                        __syncwarp();
-                        if (last) ++outs[g];
-                        if (more && (g == 0 || ni.two)) ok = issue_s(ni, nj, g);
+            uint32_t cur = describe();
+            if (cur) ok = issue_s(cur, 0) && (!(cur & kInfoTwo) || issue_s(cur, 1));
+            while (ok && cur) {
+                const int n = (int)(cur & kInfoKeys);
+                const uint32_t vt = ring_sm + vat.slot * tile_bytes;
+                uint32_t nxt = 0;
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+                    if (g == 1 && !(cur & kInfoTwo)) continue;
+                    ok = ok && warp_wait(&p_full[g], uses[g] & 1u, wc) && (g == 1 || warp_wait(&kv_full[vat.slot], vat.phase, wc)) &&
+                         // the item's first product overwrites O_g: the previous one's has been read out
+                         (!(cur & kInfoFirst) || outs[g] == 0 || warp_wait(&o_free[g], (outs[g] - 1) & 1u, wc));
+                    if (!ok) break;
+                    ++uses[g];
+                    if (g == 0 && (cur & kInfoZero)) zero_rest(ring + vat.slot * tile_bytes, n, p.chunks, lane);
+                    tc_fence_after();
+                    product_tmem<8>(tmem + kColO + g * 128, tmem + kColS + g * 128, vt, idesc_o, (n + 15) >> 4,
+                                    (cur & kInfoFirst) == 0);
+                    if (g == 1 || !(cur & kInfoTwo)) commit(&kv_empty[vat.slot]);
+                    if (cur & kInfoLast) {
+                        commit(&o_full[g]);
+                        ++outs[g];
                     }
-                    if (ok && more && ni.two && !cur.two) ok = issue_s(ni, nj, 1);
-                    vat.advance(2, p.ring);
+                    if (g == 0) nxt = describe();
+                    if (ok && nxt && (g == 0 || (nxt & kInfoTwo))) ok = issue_s(nxt, g);
                 }
-                it = it2;
+                if (ok && (nxt & kInfoTwo) && !(cur & kInfoTwo)) ok = issue_s(nxt, 1);
+                vat.advance(2, p.ring);
                 cur = nxt;
             }
-            if (elect_one()) tc_commit(&drain);
+            commit(&drain);
             __syncwarp();
             int dummy = 0;
             WaitCtx w2{&dummy, p.dev_status};
@@ -289,9 +278,22 @@ xattn_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
         const uint32_t ts = tmem + lane_base + kColS + g * 128, to = tmem + lane_base + kColO + g * 128;
         const int ochunks = (p.d + 31) >> 5;
         uint32_t uses = 0, outs = 0;
+        int q_at = 0, stored = -1;                  // Q slot of the item's first tile; slot whose output is on its way
         bool ok = true;
+        auto release = [&]() {                      // the loader may refill the slot once its output has been read
+            if (stored >= 0 && lane == 0) {
+                bulk_wait_group_read<0>();
+                mbar_arrive(&q_empty[stored]);
+            }
+            stored = -1;
+            __syncwarp();
+        };
+        Item item, following = item_of(p, blockIdx.x);      // read ahead by one item
         for (int it = blockIdx.x; ok && it < p.items; it += gridDim.x) {
-            const Item item = item_of(p, it);
+            item = following;
+            if (it + (int)gridDim.x < p.items) following = item_of(p, it + gridDim.x);
+            const int slot = (q_at + g) % kQBufs;
+            if (item.steps > 0) q_at = (q_at + (item.two ? 2 : 1)) % kQBufs;
             if (g == 1 && !item.two) continue;
             float m = -INFINITY, l = 0.0f;
             for (int j = 0; j < item.steps; ++j, ++uses) {
@@ -355,6 +357,7 @@ xattn_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&p_full[g]);
+                if (j == 0) release();
             }
             if (!ok) break;
             int head, q0;
@@ -373,6 +376,7 @@ xattn_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
             ++outs;
             tc_fence_after();
             const float inv = __frcp_rn(l);
+            uint8_t* tile = smem + slot * tile_bytes;            // its last product is done
             for (int c4 = 0; c4 < ochunks; ++c4) {
                 uint32_t o[32];
                 tmem_ld_32x32b_x32(to + c4 * 32, o);
@@ -382,19 +386,29 @@ xattn_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&o_free[g]);
                 }
-                if (row < p.Lq) {
+                uint8_t* dst = tile + (c4 >> 1) * kChunk + r * 128;
 #pragma unroll
-                    for (int i = 0; i < 32; i += 8) {
-                        if (c4 * 32 + i >= p.d) break;
-                        uint32_t w[4];
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t w[4];
 #pragma unroll
-                        for (int u = 0; u < 4; ++u)
-                            w[u] = pack_bf16(__uint_as_float(o[i + 2 * u]) * inv, __uint_as_float(o[i + 2 * u + 1]) * inv);
-                        *reinterpret_cast<uint4*>(orow + c4 * 32 + i) = make_uint4(w[0], w[1], w[2], w[3]);
-                    }
+                    for (int u = 0; u < 4; ++u)
+                        w[u] = pack_bf16(__uint_as_float(o[8 * i + 2 * u]) * inv, __uint_as_float(o[8 * i + 2 * u + 1]) * inv);
+                    *reinterpret_cast<uint4*>(dst + ((((c4 & 1) * 4 + i) ^ (r & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
                 }
             }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                if (q0 + quarter * 32 < p.Lq)
+                    for (int c = 0; c < p.chunks; ++c)
+                        tma_store_4d(&tmap_o, tile + c * kChunk + quarter * 32 * 128, c * 64, head * p.ao.h, q0 + quarter * 32,
+                                     item.b * p.ao.b);
+                bulk_commit_group();
+            }
+            stored = slot;
         }
+        release();
+        if (lane == 0) bulk_wait_group_read<0>();
     }
 
     tc_fence_before();
@@ -408,14 +422,15 @@ xattn_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
 
 cudaError_t launch_forward_tiles(const CrossAttnArgs& a, int num_sms, cudaStream_t stream) {
     FwdParams p{};
-    CUtensorMap mq, mk, mv;
+    CUtensorMap mq, mk, mv, mo;
     if (a.Lk > 0) {
         if (!make_heads_map(&mq, a.q, a.B, a.Lq, a.H, a.d, kRows, &p.aq) ||
             !make_heads_map(&mk, a.k, a.B, a.Lk, a.Hkv, a.d, kRows, &p.ak) ||
-            !make_heads_map(&mv, a.v, a.B, a.Lk, a.Hkv, a.d, kRows, &p.av))
+            !make_heads_map(&mv, a.v, a.B, a.Lk, a.Hkv, a.d, kRows, &p.av) ||
+            !make_heads_map(&mo, a.out, a.B, a.Lq, a.H, a.d, 32, &p.ao))
             return cudaErrorInvalidValue;
     } else {
-        mq = mk = mv = CUtensorMap{};               // no item has keys: nothing is loaded
+        mq = mk = mv = mo = CUtensorMap{};          // no item has keys: nothing is loaded
     }
     p.out = a.out;
     p.lse = a.lse;
@@ -439,7 +454,7 @@ cudaError_t launch_forward_tiles(const CrossAttnArgs& a, int num_sms, cudaStream
     const int smem = (kQBufs + p.ring) * tile_bytes + 1024;
     cudaError_t e = cudaFuncSetAttribute(xattn_fwd_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    xattn_fwd_kernel<<<p.items < num_sms ? p.items : num_sms, kThreads, smem, stream>>>(mq, mk, mv, p);
+    xattn_fwd_kernel<<<p.items < num_sms ? p.items : num_sms, kThreads, smem, stream>>>(mq, mk, mv, mo, p);
     e = cudaGetLastError();
     if (e == cudaSuccess) count_launch(1);
     return e;
