@@ -180,6 +180,12 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -214,6 +220,33 @@ __device__ __forceinline__ F2 mul2(F2 a, F2 b) {
     uint64_t r;
     asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(f2_bits(a.x, a.y)), "l"(f2_bits(b.x, b.y)));
     return f2_of(r);
+}
+
+// 2^x of two values on the FMA pipes, for -inf <= x < 127: x = n + r with |r| <=
+// 1/2, 2^r by the polynomial of degree 5 of least relative error (Remez exchange,
+// 2^-23.7; 2^-22.1 with the roundings of FP32), times 2^n.  Below -126 it is
+// 2^-126; NaN stays NaN.  The hardware exponential does 16 values a cycle and SM,
+// and a tile of 128 x 128 takes 1024 cycles of it: a part goes this way.
+__device__ __forceinline__ F2 ex2_fma(F2 x) {
+    asm("max.NaN.f32 %0, %0, 0fC2FC0000;" : "+f"(x.x));
+    asm("max.NaN.f32 %0, %0, 0fC2FC0000;" : "+f"(x.y));
+    const F2 m = {12583039.0f, 12583039.0f};                // 1.5 * 2^23 + 127: n + 127 in the low bits
+    const F2 t = add2(x, m);
+    const F2 u = add2(t, {-m.x, -m.y});
+    const F2 r = add2(x, {-u.x, -u.y});
+    F2 p = fma2(r, {0.0013276472454890609f, 0.0013276472454890609f}, {0.009675540961325169f, 0.009675540961325169f});
+    p = fma2(p, r, {0.05550713092088699f, 0.05550713092088699f});
+    p = fma2(p, r, {0.24022120237350464f, 0.24022120237350464f});
+    p = fma2(p, r, {0.6931469440460205f, 0.6931469440460205f});
+    p = fma2(p, r, {1.0000001192092896f, 1.0000001192092896f});
+    return mul2(p, {__uint_as_float(__float_as_uint(t.x) << 23), __uint_as_float(__float_as_uint(t.y) << 23)});
+}
+
+// 2^x of pair i of a row's values: KIND of eight pairs on the FMA pipes.
+template <int KIND>
+__device__ __forceinline__ F2 ex2_pair(F2 x, int i) {
+    if ((i * KIND & 7) + KIND >= 8 && (i & 7) != 0) return ex2_fma(x);
+    return {ex2(x.x), ex2(x.y)};
 }
 
 // The whole warp waits; false once the block gives up.

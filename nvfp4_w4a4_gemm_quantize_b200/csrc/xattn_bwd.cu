@@ -31,6 +31,9 @@ namespace xattn {
 constexpr int kBwdThreads = 640;
 constexpr int kBwdWarps = 16;                 // on a tile
 constexpr int kBwdCols = 32;                  // columns of one
+// Of eight pairs of exponentials, on the FMA pipes.  dQ and dK/dV of two clips (8192 x 512, 24 heads of 128) with 0, 2,
+// 4, 6: 170 + 203, 170 + 202, 159 + 175, 165 + 187 us.
+constexpr int kPolyPairs = 4;
 constexpr int kBwdRegsLow = 64;               // 128 x 64 + 512 x 104 <= 640 x 96
 constexpr int kBwdRegsHigh = 104;
 static_assert(128 * kBwdRegsLow + 512 * kBwdRegsHigh <= kBwdThreads * 96, "register split exceeds the launch budget");
@@ -68,19 +71,19 @@ constexpr int kDeltaThreads = 256;
 constexpr int kDeltaRows = 4;                 // rows of 16 lanes, each at once
 
 __global__ void __launch_bounds__(kDeltaThreads) delta_kernel(const nvfp4_heads grad_out, const nvfp4_heads out, float* delta,
-                                                              int64_t rows, int Lq, int H, int d) {
+                                                              int rows, int Lq, int H, int d) {
     const int lane = threadIdx.x & 15;
-    const int64_t first = ((int64_t)blockIdx.x * kDeltaThreads + threadIdx.x) / 16 * kDeltaRows;
+    const uint32_t first = blockIdx.x * (kDeltaThreads / 16 * kDeltaRows) + threadIdx.x / 16;
     uint4 a[kDeltaRows], b[kDeltaRows];
     int64_t at[kDeltaRows];
 #pragma unroll
     for (int i = 0; i < kDeltaRows; ++i) {
-        const int64_t r = first + i;                 // (b, l, h), heads innermost
+        const uint32_t r = first + i * (kDeltaThreads / 16);         // (b, l, h), heads innermost
         a[i] = b[i] = make_uint4(0, 0, 0, 0);
         at[i] = -1;
-        if (r >= rows) continue;
-        const int64_t bl = r / H, h = r - bl * H, bb = bl / Lq, l = bl - bb * Lq;
-        at[i] = (bb * H + h) * Lq + l;
+        if (r >= (uint32_t)rows) continue;
+        const uint32_t bl = r / (uint32_t)H, h = r - bl * H, bb = bl / (uint32_t)Lq, l = bl - bb * Lq;
+        at[i] = ((int64_t)bb * H + h) * Lq + l;
         if (lane * 8 < d) {
             a[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(grad_out.data) + bb * grad_out.batch_stride +
                                                         l * grad_out.token_stride + h * grad_out.head_stride + lane * 8));
@@ -415,9 +418,10 @@ xattn_dq_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
                 }
 #pragma unroll
                 for (int i = 0; i < 32; i += 2) {
-                    const F2 x = fma2({__uint_as_float(v[i]), __uint_as_float(v[i + 1])}, {p.c, p.c}, {-lse2, -lse2});
-                    v[i] = __float_as_uint(ex2(x.x));
-                    v[i + 1] = __float_as_uint(ex2(x.y));
+                    const F2 x = ex2_pair<kPolyPairs>(
+                        fma2({__uint_as_float(v[i]), __uint_as_float(v[i + 1])}, {p.c, p.c}, {-lse2, -lse2}), i / 2);
+                    v[i] = __float_as_uint(x.x);
+                    v[i + 1] = __float_as_uint(x.y);
                 }
                 if (pending) {
                     if (!(ok = read_out(prev))) break;
@@ -689,12 +693,14 @@ xattn_dkv_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const float4 l = lse4[i];                            // kept negated
-                const F2 x = fma2({__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1])}, {p.c, p.c}, {l.x, l.y});
-                const F2 y = fma2({__uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3])}, {p.c, p.c}, {l.z, l.w});
-                v[4 * i] = __float_as_uint(ex2(x.x));
-                v[4 * i + 1] = __float_as_uint(ex2(x.y));
-                v[4 * i + 2] = __float_as_uint(ex2(y.x));
-                v[4 * i + 3] = __float_as_uint(ex2(y.y));
+                const F2 x = ex2_pair<kPolyPairs>(
+                    fma2({__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1])}, {p.c, p.c}, {l.x, l.y}), 2 * i);
+                const F2 y = ex2_pair<kPolyPairs>(
+                    fma2({__uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3])}, {p.c, p.c}, {l.z, l.w}), 2 * i + 1);
+                v[4 * i] = __float_as_uint(x.x);
+                v[4 * i + 1] = __float_as_uint(x.y);
+                v[4 * i + 2] = __float_as_uint(y.x);
+                v[4 * i + 3] = __float_as_uint(y.y);
                 w[2 * i] = pack_bf16(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]));
                 w[2 * i + 1] = pack_bf16(__uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3]));
             }
@@ -879,7 +885,7 @@ cudaError_t launch_cross_attention_backward(const CrossAttnArgs& a, int num_sms,
     if (a.Lq > 0) {
         const int64_t rows = (int64_t)a.B * a.Lq * a.H;
         const int64_t per = kDeltaThreads / 16 * kDeltaRows;
-        delta_kernel<<<(unsigned)((rows + per - 1) / per), kDeltaThreads, 0, stream>>>(a.grad_out, a.out, delta, rows, a.Lq, a.H, a.d);
+        delta_kernel<<<(unsigned)((rows + per - 1) / per), kDeltaThreads, 0, stream>>>(a.grad_out, a.out, delta, (int)rows, a.Lq, a.H, a.d);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
         DqParams p{aq, ag, ak, av, ad, a.dq, a.lse, delta, a.kv_lens, a.scale * kLog2e, a.scale, a.H, a.Hkv, a.Lq, a.Lk, a.d,
                    a.H / a.Hkv, qtiles, a.B * a.H * qtiles, chunks, chunks == 1 ? 4 : 3, chunks == 1 ? 4 : 3, chunks == 1 ? 4 : 1,

@@ -197,6 +197,19 @@ def test_states_past_the_length_are_not_read(cuda_ok, Lq, junk):
 
 
 @pytest.mark.parametrize("Lq", [4, 200])
+@pytest.mark.parametrize("first", [1, 100, 128, 140, 270])
+def test_keys_of_minus_infinity(cuda_ok, Lq, first):
+    """Keys whose logits are -infinity weigh nothing, be they whole tiles."""
+    q, k, v, _ = _inputs(1, Lq, 300, 2, 2, 64, seed=17)
+    q[..., 0] = q[..., 0].abs() + 1
+    want = _reference(q, k[:, first:], v[:, first:], [300 - first], 0.125)
+    k[:, :first, :, 0] = -math.inf
+    out, lse = nv.cross_attention(q, k, v, return_lse=True)
+    _within(out, want["out"], "out")
+    _within(lse, want["lse"], "lse")
+
+
+@pytest.mark.parametrize("Lq", [4, 200])
 def test_non_finite_query_stays_in_its_row(cuda_ok, Lq):
     q, k, v, _ = _inputs(2, Lq, 90, 2, 2, 64, seed=6)
     base = nv.cross_attention(q, k, v)
