@@ -1,20 +1,32 @@
 // gemv.cu -- a few rows of activations times 4-bit weights with group scales
 // (nvfp4_gemv_w4a16):
 //   y[m,n] = g sum_k x[m,k] e2m1(w[n,k]) s[n, k / block] (+ bias[n]),  M <= 16.
-// Bound by reading the weights once, N K / 2 + N K / block bytes.
+// Bound by reading the weights once, N K / 2 + N K / block bytes, and close behind
+// by the instructions that decode them.
 //
-// The weights are the A operand of m16n8k16 products (16 output features, 8
-// rows of x), so one decoded register serves every row of x.  A block has 128
-// features (the rows of one scale atom group) and 8 warps: four over the
-// features, two over k.  A lane holds features 32 i + 8 w + lane / 4 (i < 4),
-// whose scales of 64 k are one 16-byte word of the scale layout, and of each
-// 128 k reads 16 code bytes a feature, 32 neighbouring k: the order of k within
-// a product is free as long as x comes in the same one, so nothing is shuffled.
-// x is kept in shared memory in that order.
-// The k range is split over the CTAs of a cluster (so that a matrix with few
-// features still fills the SMs); their sums are added over distributed shared
-// memory in rank order, so results do not depend on timing and need no workspace.
+// The weights are the A operand of m16n8k16 products (16 output features, 8 rows
+// of x), so one decoded register serves every row of x.  An item is 32 features x
+// 128 k: features 128 b + 8 q + (0 .. 7) + 32 (0 .. 3), whose scales of 64 k are
+// one 16-byte word of the scale layout for each lane.  A lane reads 16 code bytes
+// a feature, 32 neighbouring k: the order of k within a product is free as long as
+// x comes in the same one, so nothing is shuffled.
+// Work: a cluster of 1 to 8 blocks of 12 or 16 warps takes a range of the 32-feature
+// units; its blocks split k (each keeps its part of x in shared memory), a block's
+// warps split the block's items evenly, in order.  Sums are joined in a fixed order
+// (warps, then blocks over distributed shared memory): results do not depend on
+// timing and need no workspace.
+//
+// Decoding: the products run in FP16 where that is exact, which halves the decoding
+// instructions (the hardware has E2M1 pairs to FP16 pairs; to bf16 it takes shifts
+// and masks).  Rows of x are kept times a power of two that puts their largest
+// value (of the block's k range) at 2^14; 8 significant bits are exact in FP16 down
+// to 2^-17, so a range whose values span at most 31 binades is exact, E2M1 times
+// E4M3 is exact (6 bits, 2^-10 .. 2688), and E8M0 scales are applied relative to
+// the largest of the item's four and, in FP32, to the item's sums (after the rows' powers of two are undone, so that nothing leaves FP32's range early).  A block that finds a
+// wider range, or a value that is not finite, decodes to bf16 instead.
+#include <atomic>
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include "dit.h"
@@ -24,22 +36,26 @@
 namespace nvfp4 {
 namespace gemv {
 
-constexpr int kThreads = 256;
-constexpr int kTileN = 128;                   // features of a block
-constexpr int kWarpsK = 2;
-constexpr int kStepK = 128;                   // k of a warp's step
+// Warps of a block: as many as leave a thread the registers it needs (128, 168).
+template <int NT, bool MX>
+constexpr int kWarpsOf = NT == 1 && !MX ? 16 : 12;
+constexpr int kStepK = 128;                   // k of an item
+constexpr int kUnitN = 32;                    // features of an item
 constexpr int kMaxCluster = 8;
-constexpr int kXBytes = 72 * 1024;            // x kept at a time
+constexpr int kSmemLimit = 232448 - 2048;     // dynamic
 
 struct Params {
     GemvArgs a;
+    int units;                                // 32-feature units
     int steps;                                // ceil(K / 128)
     int segment;                              // steps of x kept at a time
+    int unit_chunk;                           // units whose sums are kept at a time
     int kb4;                                  // scale atoms along k: K / (4 block)
+    int units_each, units_more, steps_each, steps_more;     // of a cluster, of a block: the first `more` have one more
 };
 
-// One 128-k step of a lane: 16 code bytes and the scales of its four features.
-struct Step {
+// An item of a lane: 16 code bytes and the scales of its four features.
+struct Item {
     uint4 codes[4];
     uint4 sf;                                 // word i: four blocks of feature i
 };
@@ -48,6 +64,12 @@ __device__ __forceinline__ uint4 load_stream(const void* p) {
     uint4 r;
     asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
                  : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
+    return r;
+}
+
+__device__ __forceinline__ uint4 load_cached(const void* p) {
+    uint4 r;
+    asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
     return r;
 }
 
@@ -68,8 +90,16 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
     return r;
 }
 
+template <bool F16>
 __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                     uint32_t b1) {
+    if (F16) {
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                     "{%0, %1, %2, %3};"
+                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+        return;
+    }
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
                  "{%0, %1, %2, %3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -103,149 +133,450 @@ struct Scales {
     }
 };
 
-// Weights are kept times this power of two until the sums are complete.
-template <bool MX>
-constexpr float kUndo = MX ? 1.0f : 128.0f;
+// The eight E2M1 codes of a word as FP16 pairs, in order.
+__device__ __forceinline__ void decode_f16(uint32_t w, uint32_t (&h)[4]) {
+    asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3]) : "r"(w));
+}
+
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t word_of(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
+
+// One item in FP16.  NVFP4: weights times their scales, added to acc.
+template <int NT>
+__device__ __forceinline__ void item_f16_nvfp4(const Item& it, const uint8_t* const (&xrow)[NT], int t, float (&acc)[2][NT][4]) {
+    uint32_t sc[4][2];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint32_t h;
+        const uint16_t two = (uint16_t)((word_of(it.sf, i) >> (16 * (t & 1))) & 0x7F7Fu);
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(two));
+        sc[i][0] = __byte_perm(h, 0, 0x1010);
+        sc[i][1] = __byte_perm(h, 0, 0x3232);
+    }
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+        uint4 b[NT];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) b[j] = *reinterpret_cast<const uint4*>(xrow[j] + w * 64);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            uint32_t f[2][4];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                decode_f16(word_of(it.codes[2 * u + i], w), f[i]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) f[i][e] = mul_f16x2(f[i][e], sc[2 * u + i][w >> 1]);
+            }
+#pragma unroll
+            for (int half = 0; half < 2; ++half)
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+                    mma<true>(acc[u][j], f[0][2 * half], f[1][2 * half], f[0][2 * half + 1], f[1][2 * half + 1], half ? b[j].z : b[j].x,
+                              half ? b[j].w : b[j].y);
+        }
+    }
+}
+
+// MX: weights times 2^(their scale's byte - the item's largest, of the feature), the sums times 2^(that - 128).  Lanes
+// of a column share no block, so a lane has one scale a feature.  Where a block is more than 2^23 below the largest
+// (E2M1 would leave FP16), the item runs once per block, the others' codes as zeros.
+template <int NT, bool WIDE>
+__device__ __forceinline__ void item_f16_mx(const Item& it, const uint8_t* const (&xrow)[NT], int t, const uint32_t (&top)[4],
+                                            const uint32_t (&mine)[4], const float (&undo)[NT][2], float (&acc)[2][NT][4]) {
+#pragma unroll 1
+    for (int only = WIDE ? 0 : 4; only < (WIDE ? 4 : 5); ++only) {
+        uint32_t sc[4];
+        float whole[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t at = only < 4 ? (word_of(it.sf, i) >> (8 * only)) & 0xFFu : top[i];
+            const uint32_t down = only < 4 ? 0u : top[i] - mine[i];            // FP16 2^-down, subnormal past 14
+            const uint32_t h = __half_as_ushort(__float2half_rn(__uint_as_float((127u - down) << 23)));
+            sc[i] = only < 4 && only != t ? 0u : h * 0x10001u;
+            whole[i] = __uint_as_float(at > 1u ? (at - 1u) << 23 : 0x00200000u << at);      // 2^(at - 128)
+        }
+        float sum[2][NT][4] = {};
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            uint4 b[NT];
+#pragma unroll
+            for (int j = 0; j < NT; ++j) b[j] = *reinterpret_cast<const uint4*>(xrow[j] + w * 64);
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                uint32_t f[2][4];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    decode_f16(word_of(it.codes[2 * u + i], w), f[i]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) f[i][e] = mul_f16x2(f[i][e], sc[2 * u + i]);
+                }
+#pragma unroll
+                for (int half = 0; half < 2; ++half)
+#pragma unroll
+                    for (int j = 0; j < NT; ++j)
+                        mma<true>(sum[u][j], f[0][2 * half], f[1][2 * half], f[0][2 * half + 1], f[1][2 * half + 1], half ? b[j].z : b[j].x,
+                                  half ? b[j].w : b[j].y);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    acc[u][j][e] = fmaf(sum[u][j][e] * undo[j][e & 1], whole[2 * u + (e >> 1)], acc[u][j][e]);
+    }
+}
+
+// The item of a wide spread, out of line: nothing of it stays in registers where it is not called.
+template <int NT>
+__device__ __noinline__ void item_f16_mx_wide(const Item* it, const uint8_t* const* xrow, int t, const float* back, float* acc) {
+    const uint32_t none[4] = {0, 0, 0, 0};
+    float undo[NT][2];
+#pragma unroll
+    for (int i = 0; i < 2 * NT; ++i) (&undo[0][0])[i] = back[i];
+    const uint8_t* xr[NT];
+    float sum[2][NT][4];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) xr[j] = xrow[j];
+#pragma unroll
+    for (int i = 0; i < 8 * NT; ++i) (&sum[0][0][0])[i] = acc[i];
+    item_f16_mx<NT, true>(*it, xr, t, none, none, undo, sum);
+#pragma unroll
+    for (int i = 0; i < 8 * NT; ++i) acc[i] = (&sum[0][0][0])[i];
+}
+
+// One item in bf16: x pairs in the order (0,4) (1,5) (2,6) (3,7) of a code word.
+template <int NT, bool MX>
+__device__ __noinline__ void item_bf16(const Item* from, const uint8_t* const* xrow, int t, float* sums) {
+    const Item it = *from;
+    float acc[2][NT][4];
+#pragma unroll
+    for (int i = 0; i < 8 * NT; ++i) (&acc[0][0][0])[i] = sums[i];
+    Scales<MX> sc[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sc[i].set(word_of(it.sf, i), t);
+    const bool over =
+        MX && __any_sync(0xffffffffu, ((sc[0].over | sc[1].over | sc[2].over | sc[3].over) & 0x7FFFu) != 0x3F80u);
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+        uint4 b[NT];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) b[j] = *reinterpret_cast<const uint4*>(xrow[j] + w * 64);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            uint32_t f[4][2];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t c = word_of(it.codes[i], w);
+                const uint32_t sv = sc[i].s[w >> 1];
+                f[i][0] = mul_bf16x2(half ? spread<2>(c) : spread<0>(c), sv);
+                f[i][1] = mul_bf16x2(half ? spread<3>(c) : spread<1>(c), sv);
+                if (over) {
+                    f[i][0] = mul_bf16x2(f[i][0], sc[i].over);
+                    f[i][1] = mul_bf16x2(f[i][1], sc[i].over);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                const uint32_t b0 = half ? b[j].z : b[j].x, b1 = half ? b[j].w : b[j].y;
+                mma<false>(acc[0][j], f[0][0], f[1][0], f[0][1], f[1][1], b0, b1);
+                mma<false>(acc[1][j], f[2][0], f[3][0], f[2][1], f[3][1], b0, b1);
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 8 * NT; ++i) sums[i] = (&acc[0][0][0])[i];
+}
 
 template <int NT, bool MX>
-__global__ void __launch_bounds__(kThreads, 2) gemv_kernel(const Params p) {
-    extern __shared__ __align__(16) uint8_t xs[];           // [M][segment][4][4] 16-byte pieces of x (+ 64 bytes a row)
-    __shared__ float part[NT * 8][kTileN];                  // this CTA's sums
+__global__ void __launch_bounds__(32 * kWarpsOf<NT, MX>, 1) gemv_kernel(const Params p) {
+    constexpr int kWarps = kWarpsOf<NT, MX>, kThreads = 32 * kWarps;
+    constexpr int kAhead = NT == 2 && MX ? 1 : 2;           // items on their way while one is computed, as registers allow
+    extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ uint32_t x_max[16], x_min[16];               // of a row's k range: largest |x|, smallest nonzero |x| - 1, as bits
+    __shared__ int head_unit[kWarps];                       // the unit a warp starts inside of, or -1
+    constexpr int kEarly = NT == 1 ? 2 : 1;                             // pieces of x a thread loads before the first weights
 
     const GemvArgs& a = p.a;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int wn = warp & 3, wk = warp >> 2;
     const int rank = (int)cluster_ctarank(), ranks = gridDim.y;
-    const int nb = blockIdx.x;
-    const int first = (int)((int64_t)p.steps * rank / ranks), last = (int)((int64_t)p.steps * (rank + 1) / ranks);
+    const int c = blockIdx.x;
+    const int u_first = c * p.units_each + min(c, p.units_more), u_last = u_first + p.units_each + (c < p.units_more ? 1 : 0);
+    const int k_first = rank * p.steps_each + min(rank, p.steps_more), k_last = k_first + p.steps_each + (rank < p.steps_more ? 1 : 0);
     const int row_bytes = p.segment * 256 + 64;
+    uint8_t* const xs = smem;                               // [M][segment][4][4] 16-byte pieces of x (+ 64 bytes a row)
+    float* const part = reinterpret_cast<float*>(smem + a.M * row_bytes);      // [unit_chunk][M][32]: sums
+    float* const heads = part + p.unit_chunk * kUnitN * a.M;                   // [warp][M][32]: sums of units begun by another warp
+    const int unit_floats = kUnitN * a.M;
+    const int64_t row_codes = a.K / 2;
 
-    // this lane's features and, within a step, its 32 k
-    const uint8_t* codes[4];
-    uint32_t have = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int n = nb * kTileN + 32 * i + 8 * wn + g;
-        have |= (n < a.N ? 1u : 0u) << i;
-        codes[i] = a.w_codes + (int64_t)(n < a.N ? n : 0) * (a.K / 2) + 16 * t;
-    }
-    const uint8_t* sf = a.w_sf + (int64_t)nb * p.kb4 * 512 + (8 * wn + g) * 16;
-    auto fetch = [&](int s, Step& st) {
-        const bool in = s < last && s * kStepK + 32 * t < a.K;      // a last half step has no k for t >= 2
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            st.codes[i] = in && (have >> i & 1u) ? load_stream(codes[i] + (int64_t)s * 64) : make_uint4(0, 0, 0, 0);
-        st.sf = in ? load_stream(sf + (int64_t)(MX ? s : 2 * s + (t >> 1)) * 512) : make_uint4(0, 0, 0, 0);
-    };
-
-    float acc[2][NT][4] = {};
-    Step cur, nxt;
-    int s = first + wk;
-    fetch(s, cur);
     const uint8_t* xrow[NT];
 #pragma unroll
     for (int j = 0; j < NT; ++j) xrow[j] = xs + min(8 * j + g, a.M - 1) * row_bytes + t * 16;
 
-    for (int seg = first; seg < last; seg += p.segment) {
-        const int seg_end = min(seg + p.segment, last);
-        if (seg != first) __syncthreads();
-        // x of the segment, eight values a piece in the order (0,4) (1,5) (2,6) (3,7) of a code word;
-        // piece i of lane column t of a step sits at i * 64 + t * 16 (conflict-free reads)
-        const int pieces = (seg_end - seg) * 16;
-        for (int i = threadIdx.x; i < pieces * a.M; i += kThreads) {
-            const int m = i / pieces, q = i - m * pieces, k = seg * kStepK + q * 8;
-            uint4 v = make_uint4(0, 0, 0, 0), o;
-            if (k < a.K) v = __ldg(reinterpret_cast<const uint4*>(a.x + (int64_t)m * a.ld_x + k));
-            o.x = __byte_perm(v.x, v.z, 0x5410);
-            o.y = __byte_perm(v.x, v.z, 0x7632);
-            o.z = __byte_perm(v.y, v.w, 0x5410);
-            o.w = __byte_perm(v.y, v.w, 0x7632);
-            *reinterpret_cast<uint4*>(xs + m * row_bytes + (q >> 4) * 256 + (q & 3) * 64 + ((q >> 2) & 3) * 16) = o;
-        }
-        __syncthreads();
-        for (; s < seg_end; s += kWarpsK) {
-            fetch(s + kWarpsK, nxt);
-            Scales<MX> sc[4];
-            const uint32_t sfw[4] = {cur.sf.x, cur.sf.y, cur.sf.z, cur.sf.w};
+    for (int u0 = u_first; u0 < u_last; u0 += p.unit_chunk) {
+        const int units = min(p.unit_chunk, u_last - u0);
+        for (int k0 = k_first; k0 < k_last; k0 += p.segment) {
+            const int steps = min(p.segment, k_last - k0);
+            const int total = units * steps;
+            int item = total / kWarps * warp + min(warp, total % kWarps);
+            const int end = item + total / kWarps + (warp < total % kWarps ? 1 : 0);
+
+            // the next items' weights
+            int fu = item / steps, fk = item - fu * steps, left = end - item;
+            const uint8_t *codes = nullptr, *sf = nullptr;
+            uint32_t have = 0;
+            auto aim = [&]() {
+                const int u = u0 + fu, n = (u >> 2) * 128 + (u & 3) * 8 + g;
+                have = 0;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) sc[i].set(sfw[i], t);
-            const bool over = MX && __any_sync(0xffffffffu, ((sc[0].over | sc[1].over | sc[2].over | sc[3].over) & 0x7FFFu) != 0x3F80u);
+                for (int i = 0; i < 4; ++i) have |= (n + 32 * i < a.N ? 1u : 0u) << i;
+                codes = a.w_codes + (int64_t)n * row_codes + 16 * t;
+                sf = a.w_sf + (int64_t)(u >> 2) * p.kb4 * 512 + ((u & 3) * 8 + g) * 16;
+            };
+            auto fetch = [&](Item& it) {
+                if (left <= 0) return;
+                const int s = k0 + fk;
+                const bool in = s * kStepK + 32 * t < a.K;  // a last half step has no k for t >= 2
 #pragma unroll
-            for (int w = 0; w < 4; ++w) {
-                uint4 b[NT];
+                for (int i = 0; i < 4; ++i)
+                    it.codes[i] = in && (have >> i & 1u) ? load_stream(codes + i * 32 * row_codes + (int64_t)s * 64)
+                                                         : make_uint4(0, 0, 0, 0);
+                it.sf = in ? load_stream(sf + (int64_t)(MX ? s : 2 * s + (t >> 1)) * 512) : make_uint4(0, 0, 0, 0);
+                --left;
+                if (++fk == steps) {
+                    fk = 0;
+                    ++fu;
+                    if (left > 0) aim();
+                }
+            };
+            // x of the k range (several warps a row, or several rows a warp), its first loads ahead of the weights'
+            const int per_row = max(1, kWarps / a.M), pieces = steps * 16;     // warps of a row
+            const int p_first = (warp % per_row) * 32 + lane, p_step = per_row * 32;
+            const int m_first = warp / per_row, m_step = kWarps / per_row;
+            auto piece = [&](int m, int q) {
+                return reinterpret_cast<uint4*>(xs + m * row_bytes + (q >> 4) * 256 + (q & 3) * 64 + ((q >> 2) & 3) * 16);
+            };
+            auto load_x = [&](int m, int q) {
+                const int k = k0 * kStepK + q * 8;
+                return q < pieces && k < a.K ? load_cached(a.x + (int64_t)m * a.ld_x + k) : make_uint4(0, 0, 0, 0);
+            };
+            uint4 early[kEarly];
 #pragma unroll
-                for (int j = 0; j < NT; ++j) b[j] = *reinterpret_cast<const uint4*>(xrow[j] + (s - seg) * 256 + w * 64);
+            for (int i = 0; i < kEarly; ++i) early[i] = m_first < a.M ? load_x(m_first, p_first + i * p_step) : make_uint4(0, 0, 0, 0);
+            int unit = fu, step = fk;
+            const bool begins = fk == 0, some = item < end;
+            Item queue[kAhead + 1];
+            if (left > 0) aim();
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    uint32_t f[4][2];
+            for (int i = 0; i < kAhead; ++i) fetch(queue[i]);
+
+            if (u0 != u_first || k0 != k_first) __syncthreads();
+            if (threadIdx.x < 16) {
+                x_max[threadIdx.x] = 0;
+                x_min[threadIdx.x] = 0xFFFFu;
+            }
+            if (lane == 0) head_unit[warp] = some && !begins ? unit : -1;
+            __syncthreads();
+            for (int m = m_first; m < a.M; m += m_step) {
+                uint32_t hi = 0, lo = 0xFFFFFFFFu;
+                auto take = [&](int q, const uint4& v) {
+                    *piece(m, q) = v;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const uint32_t c = w == 0 ? cur.codes[i].x : w == 1 ? cur.codes[i].y : w == 2 ? cur.codes[i].z : cur.codes[i].w;
-                        const uint32_t sv = sc[i].s[w >> 1];
-                        f[i][0] = mul_bf16x2(half ? spread<2>(c) : spread<0>(c), sv);
-                        f[i][1] = mul_bf16x2(half ? spread<3>(c) : spread<1>(c), sv);
-                        if (over) {
-                            f[i][0] = mul_bf16x2(f[i][0], sc[i].over);
-                            f[i][1] = mul_bf16x2(f[i][1], sc[i].over);
-                        }
+                        const uint32_t b = word_of(v, i) & 0x7FFF7FFFu;
+                        hi = __vmaxu2(hi, b);
+                        lo = __vminu2(lo, __vsub2(b, 0x00010001u));
                     }
+                };
+                int q = p_first;
+                if (m == m_first)
 #pragma unroll
-                    for (int j = 0; j < NT; ++j) {
-                        const uint32_t b0 = half ? b[j].z : b[j].x, b1 = half ? b[j].w : b[j].y;
-                        mma(acc[0][j], f[0][0], f[1][0], f[0][1], f[1][1], b0, b1);
-                        mma(acc[1][j], f[2][0], f[3][0], f[2][1], f[3][1], b0, b1);
-                    }
+                    for (int i = 0; i < kEarly; ++i, q += p_step)
+                        if (q < pieces) take(q, early[i]);
+                constexpr int kBatch = 5;
+                for (; q < pieces; q += kBatch * p_step) {
+                    uint4 v[kBatch];
+#pragma unroll
+                    for (int i = 0; i < kBatch; ++i) v[i] = load_x(m, q + i * p_step);
+#pragma unroll
+                    for (int i = 0; i < kBatch; ++i)
+                        if (q + i * p_step < pieces) take(q + i * p_step, v[i]);
+                }
+                hi = __reduce_max_sync(0xffffffffu, max(hi & 0xFFFFu, hi >> 16));
+                lo = __reduce_min_sync(0xffffffffu, min(lo & 0xFFFFu, lo >> 16));
+                if (lane == 0) {
+                    atomicMax(&x_max[m], hi);
+                    atomicMin(&x_min[m], lo);
                 }
             }
-            cur = nxt;
-        }
-    }
+            __syncthreads();
+            bool fits = true;                               // every row within FP16's exact range
+            for (int i = 0; i < a.M; ++i) {
+                const int top = (int)(x_max[i] >> 7), low = (int)((x_min[i] + 1) >> 7);
+                fits = fits && (x_max[i] == 0 || (top >= 64 && top <= 190 && low >= top - 31));
+            }
+            for (int m = m_first; m < a.M; m += m_step) {
+                const int top = (int)(x_max[m] >> 7);
+                const float by = x_max[m] ? __uint_as_float((uint32_t)(127 + 14 + 127 - top) << 23) : 1.0f;
+                for (int q = p_first; q < pieces; q += p_step) {
+                    const uint4 v = *piece(m, q);
+                    uint32_t o[4];
+                    if (fits) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const uint32_t w = word_of(v, i);
+                            const __half2 h = __floats2half2_rn(__uint_as_float(w << 16) * by, __uint_as_float(w & 0xFFFF0000u) * by);
+                            o[i] = *reinterpret_cast<const uint32_t*>(&h);
+                        }
+                    } else {
+                        o[0] = __byte_perm(v.x, v.z, 0x5410);
+                        o[1] = __byte_perm(v.x, v.z, 0x7632);
+                        o[2] = __byte_perm(v.y, v.w, 0x5410);
+                        o[3] = __byte_perm(v.y, v.w, 0x7632);
+                    }
+                    *piece(m, q) = make_uint4(o[0], o[1], o[2], o[3]);
+                }
+            }
+            __syncthreads();
 
-    // the two k halves of the block, then the cluster's CTAs, in a fixed order
+            float undo[NT][2];                              // of this lane's rows' powers of two
 #pragma unroll
-    for (int h = kWarpsK - 1; h >= 0; --h) {
-        if (wk == h) {
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
+            for (int i = 0; i < 2 * NT; ++i) {
+                const uint32_t top = x_max[8 * (i >> 1) + 2 * t + (i & 1)] >> 7;
+                undo[i >> 1][i & 1] = fits && top ? __uint_as_float((top - 14u) << 23) : 1.0f;
+            }
+            float acc[2][NT][4] = {};
+            bool first_unit = true;
+            auto flush = [&]() {                            // sums of the unit, in units of x and the weights
+                const bool head = first_unit && !begins;
+                float* dst = head ? heads + warp * unit_floats : part + unit * unit_floats;
+                const bool add = !head && k0 != k_first;
 #pragma unroll
                 for (int j = 0; j < NT; ++j)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        float* d = &part[8 * j + 2 * t + (e & 1)][32 * (2 * u + (e >> 1)) + 8 * wn + g];
-                        *d = h == kWarpsK - 1 ? acc[u][j][e] : *d + acc[u][j][e];
+                    for (int c = 0; c < 2; ++c) {
+                        const int row = 8 * j + 2 * t + c;
+                        if (row >= a.M) continue;
+                        // the bf16 path's NVFP4 weights are 2^-7 of theirs, the FP16 path's E8M0 scales half of theirs
+                        const float by = fits ? (MX ? 2.0f : undo[j][c]) : (MX ? 1.0f : 128.0f);
+#pragma unroll
+                        for (int u = 0; u < 2; ++u)
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                float* at = dst + row * kUnitN + 8 * (2 * u + h) + g;
+                                const float v = acc[u][j][2 * h + c] * by;
+                                *at = add ? *at + v : v;
+                                acc[u][j][2 * h + c] = 0.0f;
+                            }
                     }
+                first_unit = false;
+            };
+            auto run = [&](Item& it) {
+                const uint8_t* xr[NT];
+#pragma unroll
+                for (int j = 0; j < NT; ++j) xr[j] = xrow[j] + step * 256;
+                uint32_t top[4], mine[4];
+                bool wide = false;
+                if (MX) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t s = word_of(it.sf, i), m = __vmaxu4(s, s >> 16);
+                        mine[i] = (s >> (8 * t)) & 0xFFu;
+                        top[i] = max(m & 0xFFu, (m >> 8) & 0xFFu);
+                        wide = wide || top[i] - mine[i] > 23u;
+                    }
+                    wide = __any_sync(0xffffffffu, wide);
+                }
+                if (!fits || wide) {
+                    const Item copy = it;
+                    float sums[8 * NT];
+#pragma unroll
+                    for (int i = 0; i < 8 * NT; ++i) sums[i] = (&acc[0][0][0])[i];
+                    if (!fits) item_bf16<NT, MX>(&copy, xr, t, sums);
+                    else {
+                        float back[2 * NT];
+#pragma unroll
+                        for (int i = 0; i < 2 * NT; ++i) back[i] = (&undo[0][0])[i];
+                        item_f16_mx_wide<NT>(&copy, xr, t, back, sums);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 8 * NT; ++i) (&acc[0][0][0])[i] = sums[i];
+                } else if (MX) {
+                    item_f16_mx<NT, false>(it, xr, t, top, mine, undo, acc);
+                } else {
+                    item_f16_nvfp4<NT>(it, xr, t, acc);
+                }
+                ++item;
+                if (++step == steps) {
+                    flush();
+                    step = 0;
+                    ++unit;
+                }
+            };
+            while (item < end) {
+#pragma unroll
+                for (int i = 0; i <= kAhead; ++i) {
+                    fetch(queue[(i + kAhead) % (kAhead + 1)]);
+                    if (item < end) run(queue[i]);
+                }
+            }
+            if (some && step != 0) flush();
+            __syncthreads();
+            // what warps added to units that another one began, in the warps' order; a warp takes every kWarps-th unit
+            for (int w = 1; w < kWarps; ++w) {
+                const int u = head_unit[w];
+                if (u < 0 || u % kWarps != warp) continue;
+                for (int i = lane; i < unit_floats; i += 32) part[u * unit_floats + i] += heads[w * unit_floats + i];
+            }
         }
-        __syncthreads();
+        if (ranks > 1) cluster_sync_all();
+        else __syncthreads();
+        // the blocks' sums, in rank order; each block finishes a part of the features
+        const float scale = a.w_scale ? __ldg(a.w_scale) : 1.0f;
+        const int floats = units * unit_floats;
+        const int share = (floats + ranks - 1) / ranks, f_first = share * rank, f_last = min(f_first + share, floats);
+        for (int i = f_first + threadIdx.x; i < f_last; i += kThreads) {
+            const int u = i / unit_floats, r = i - u * unit_floats, row = r / kUnitN, f = r & (kUnitN - 1);
+            const int n = ((u0 + u) >> 2) * 128 + ((u0 + u) & 3) * 8 + (f >> 3) * 32 + (f & 7);
+            float v = 0.0f;
+            if (ranks > 1) {
+                const uint32_t at = smem_u32(part + i);
+                for (int q = 0; q < ranks; ++q) {
+                    float x;
+                    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(mapa_shared(at, (uint32_t)q)));
+                    v += x;
+                }
+            } else {
+                v = part[i];
+            }
+            if (n < a.N) {
+                v *= scale;
+                if (a.bias) v += __ldg(a.bias + n);
+                if (a.y_f32) static_cast<float*>(a.y)[(int64_t)row * a.N + n] = v;
+                else static_cast<__nv_bfloat16*>(a.y)[(int64_t)row * a.N + n] = __float2bfloat16_rn(v);
+            }
+        }
+        if (ranks > 1) cluster_sync_all();                  // the others may still read this block's sums
     }
-    if (ranks > 1) cluster_sync_all();
-    const float scale = (a.w_scale ? __ldg(a.w_scale) : 1.0f) * kUndo<MX>;
-    const int share = kTileN / ranks;                       // features this CTA finishes
-    for (int i = threadIdx.x; i < share * a.M; i += kThreads) {
-        const int m = i / share, c = rank * share + i - m * share, n = nb * kTileN + c;
-        const uint32_t at = smem_u32(&part[m][c]);
-        float v = 0.0f;
-        for (int r = 0; r < ranks; ++r) {
-            float q;
-            asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(q) : "r"(mapa_shared(at, (uint32_t)r)));
-            v += q;
-        }
-        if (n < a.N) {
-            v *= scale;
-            if (a.bias) v += __ldg(a.bias + n);
-            if (a.y_f32) static_cast<float*>(a.y)[(int64_t)m * a.N + n] = v;
-            else static_cast<__nv_bfloat16*>(a.y)[(int64_t)m * a.N + n] = __float2bfloat16_rn(v);
-        }
-    }
-    if (ranks > 1) cluster_sync_all();                      // the others may still read this CTA's sums
 }
 
 template <int NT, bool MX>
-cudaError_t launch(const Params& p, int blocks, int ranks, int smem, cudaStream_t stream) {
+cudaError_t launch(const Params& p, int clusters, int ranks, int smem, cudaStream_t stream) {
     cudaError_t e = cudaFuncSetAttribute(gemv_kernel<NT, MX>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)blocks, (unsigned)ranks);
-    cfg.blockDim = dim3(kThreads);
+    cfg.gridDim = dim3((unsigned)clusters, (unsigned)ranks);
+    cfg.blockDim = dim3(32 * kWarpsOf<NT, MX>);
     cfg.dynamicSmemBytes = (size_t)smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr;
@@ -254,10 +585,42 @@ cudaError_t launch(const Params& p, int blocks, int ranks, int smem, cudaStream_
     attr.val.clusterDim.y = (unsigned)ranks;
     attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = ranks > 1 ? 1 : 0;
     e = cudaLaunchKernelEx(&cfg, gemv_kernel<NT, MX>, p);
     if (e == cudaSuccess) count_launch(1);
     return e;
+}
+
+// Clusters of `ranks` blocks (one block an SM) that the device runs at once: asked for once per device.
+int64_t resident_clusters(bool two, bool mx, int ranks, int num_sms) {
+    if (ranks <= 2) return num_sms / ranks;
+    static std::atomic<int> known[64][2];                   // for four, eight blocks
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 1;
+    std::atomic<int>& slot = known[dev][ranks == 8];
+    int n = slot.load(std::memory_order_relaxed);
+    if (n == 0) {
+        const void* kernel = two ? (mx ? (const void*)gemv_kernel<2, true> : (const void*)gemv_kernel<2, false>)
+                                 : (mx ? (const void*)gemv_kernel<1, true> : (const void*)gemv_kernel<1, false>);
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit) != cudaSuccess) return 1;
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3((unsigned)num_sms, (unsigned)ranks);
+        cfg.blockDim = dim3(!two && !mx ? 32 * kWarpsOf<1, false> : 32 * kWarpsOf<2, true>);
+        cfg.dynamicSmemBytes = kSmemLimit;
+        cudaLaunchAttribute attr;
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = 1;
+        attr.val.clusterDim.y = (unsigned)ranks;
+        attr.val.clusterDim.z = 1;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+        if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1) {
+            (void)cudaGetLastError();
+            return 1;
+        }
+        slot.store(n, std::memory_order_relaxed);
+    }
+    return n;
 }
 
 }  // namespace gemv
@@ -266,21 +629,42 @@ cudaError_t launch_gemv(const GemvArgs& a, int num_sms, cudaStream_t stream) {
     using namespace gemv;
     Params p{};
     p.a = a;
+    p.units = (a.N + 127) / 128 * 4;
     p.steps = (a.K + kStepK - 1) / kStepK;
     p.kb4 = a.K / (a.mx ? 128 : 64);
-    const int blocks = (a.N + kTileN - 1) / kTileN;
-    // as many CTAs along k as leave every warp a step, until the SMs hold four blocks each
-    int ranks = 1;
-    while (ranks < kMaxCluster && p.steps >= 2 * ranks * kWarpsK && blocks * ranks < 4 * num_sms) ranks *= 2;
-    const int per_rank = (p.steps + ranks - 1) / ranks;
-    p.segment = (kXBytes / a.M - 64) / 256;
-    if (p.segment > per_rank) p.segment = per_rank;
-    // whole rounds of the block's warps, so that each warp's next step stays its own
-    if (p.segment > kWarpsK) p.segment -= p.segment % kWarpsK;
-    const int smem = a.M * (p.segment * 256 + 64);
+    // Blocks along k: the number that ends first, in items of a warp; a cluster's start and join cost about two, a block
+    // reads its part of x first.  The clusters all run at once: more of them than the GPCs hold would double the time.
+    const int warps = a.M <= 8 && !a.mx ? kWarpsOf<1, false> : kWarpsOf<2, true>;
+    int ranks = 1, clusters = 1;
+    int64_t best = 0;
+    for (int r = 1; r <= kMaxCluster && r <= p.steps; r *= 2) {
+        const int64_t most = resident_clusters(a.M > 8, a.mx, r, num_sms);
+        const int64_t c = p.units < most ? p.units : most;
+        const int64_t per = (p.units + c - 1) / c, steps = (p.steps + r - 1) / r;
+        const int64_t cost = 16 * ((per * steps + warps - 1) / warps + (r > 1 ? 2 : 0)) + a.M * steps / 9;
+        if (best == 0 || cost < best) {
+            best = cost;
+            ranks = r;
+            clusters = (int)c;
+        }
+    }
+    p.units_each = p.units / clusters;
+    p.units_more = p.units % clusters;
+    p.steps_each = p.steps / ranks;
+    p.steps_more = p.steps % ranks;
+    const int steps = (p.steps + ranks - 1) / ranks;
+    const int unit_bytes = kUnitN * a.M * 4;
+    // shared memory: x of a k segment (at most 96 KB), the warps' heads, the sums of as many units as are left room for
+    p.segment = (96 * 1024 / a.M - 64) / 256;
+    if (p.segment > steps) p.segment = steps;
+    const int x_bytes = a.M * (p.segment * 256 + 64);
+    const int per = (p.units + clusters - 1) / clusters;
+    p.unit_chunk = (kSmemLimit - x_bytes - warps * unit_bytes) / unit_bytes;
+    if (p.unit_chunk > per) p.unit_chunk = per;
+    const int smem = x_bytes + (warps + p.unit_chunk) * unit_bytes;
     if (a.M <= 8)
-        return a.mx ? launch<1, true>(p, blocks, ranks, smem, stream) : launch<1, false>(p, blocks, ranks, smem, stream);
-    return a.mx ? launch<2, true>(p, blocks, ranks, smem, stream) : launch<2, false>(p, blocks, ranks, smem, stream);
+        return a.mx ? launch<1, true>(p, clusters, ranks, smem, stream) : launch<1, false>(p, clusters, ranks, smem, stream);
+    return a.mx ? launch<2, true>(p, clusters, ranks, smem, stream) : launch<2, false>(p, clusters, ranks, smem, stream);
 }
 
 }  // namespace nvfp4
