@@ -7,7 +7,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libnvfp4.so")
 SOURCES = ["api.cu", "quantize.cu", "quantize_noalloc.cu", "layernorm.cu", "mx.cu", "blocksize.cu", "attn.cu", "gemm_w4a4.cu",
-           "gemm_w4a4_2sm.cu", "gemm_w4a16.cu", "api_dit.cu", "gemv.cu", "rotary.cu", "xattn_fwd.cu", "xattn_bwd.cu"]
+           "gemm_w4a4_2sm.cu", "gemm_w4a16.cu", "api_dit.cu", "gemv.cu", "rotary.cu", "xattn_fwd.cu", "xattn_few.cu", "xattn_bwd.cu"]
 HEADERS = ["ptx.cuh", "quant_math.cuh", "epilogue.cuh", "internal.h", "gemm.h", "tmap.h", "dit.h", "xattn.cuh"]
 INCLUDES = [os.path.join(os.path.dirname(HERE), "include", f) for f in ("nvfp4.h", "nvfp4_dit.h")]
 

@@ -52,6 +52,9 @@ struct CrossAttnArgs {
     void* workspace;
 };
 
+namespace xattn {
+cudaError_t launch_forward_few(const CrossAttnArgs& a, int num_sms, cudaStream_t stream);      // at most 16 rows a key / value head
+}
 cudaError_t launch_cross_attention(const CrossAttnArgs& a, int num_sms, cudaStream_t stream);
 cudaError_t launch_cross_attention_backward(const CrossAttnArgs& a, int num_sms, cudaStream_t stream);
 size_t cross_attention_backward_workspace(int64_t B, int64_t H, int64_t Hkv, int64_t Lq, int64_t Lk, int64_t d);

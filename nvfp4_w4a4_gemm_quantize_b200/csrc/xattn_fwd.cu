@@ -475,6 +475,8 @@ cudaError_t launch_forward_tiles(const CrossAttnArgs& a, int num_sms, cudaStream
 }  // namespace xattn
 
 cudaError_t launch_cross_attention(const CrossAttnArgs& a, int num_sms, cudaStream_t stream) {
+    // at most 16 rows a key / value head: a tile of 128 would be mostly empty, and its keys in one block's hands
+    if ((int64_t)a.H / a.Hkv * a.Lq <= 16) return xattn::launch_forward_few(a, num_sms, stream);
     return xattn::launch_forward_tiles(a, num_sms, stream);
 }
 
