@@ -1,11 +1,15 @@
 // rotary.cu -- rotary positions with several axes (nvfp4_rotary).
 //
 // Pair j of a token's head turns by angle[token, j] = position[axis(j)] *
-// theta^(-2 i / width(axis)); the angles do not depend on the head, so a block
-// takes a few tokens, forms their cos / sin once in shared memory and turns
-// every head with them.  The angle is formed in turns (the frequencies come
-// divided by 2 pi, in FP64 from the host) and reduced to half a turn in FP64:
-// three FP64 operations per token and pair, against 2 H elements moved.
+// theta^(-2 i / width(axis)); the angles do not depend on the head.  A block takes
+// a few tokens and forms their cos / sin once in shared memory; a thread has one
+// place (a 16-byte vector, or one in each half) of one token's heads, reads its
+// angles once and turns that place in several heads, all loaded ahead.  (With a
+// place per vector and its angles read for each, it was bound by those reads and
+// the addresses: 177 instructions a vector, 100 us for 32768 x 24 x 128.)
+// The angle is formed in turns (the frequencies come divided by 2 pi, in FP64 from
+// the host) and reduced to half a turn in FP64: three FP64 operations per token and
+// pair, against 2 H elements moved.
 // Bound by memory: every element is read and written once.
 #include <cmath>
 #include <cuda_bf16.h>
@@ -18,12 +22,11 @@ namespace nvfp4 {
 namespace rotary {
 
 constexpr int kThreads = 256;
-constexpr int kAhead = 4;                 // vectors a thread loads before it waits for the angles
-constexpr int kMaxTokens = 32;            // tokens of a block
+constexpr int kHeads = 8;                 // heads of a thread (4 with split pairs, two vectors each)
 
 // n / d for 0 <= n < 2^31 as a multiplication (d >= 1): m = ceil(2^(31 + s) / d), 2^s >= d.
 struct FastDiv {
-    uint32_t d, m, s;                     // H d <= 2^26 (checked by the entry point), so 32 tokens stay below 2^31
+    uint32_t d, m, s;                     // used for n < 256 only
 };
 
 FastDiv fast_div(uint32_t d) {
@@ -44,7 +47,7 @@ struct Params {
     bool pos_f32;
     int L, H, pairs;
     int tokens, tiles;                    // tokens of a block, blocks of a sample
-    FastDiv units, heads_units;           // vectors of a head, of a token
+    FastDiv units, splits;                // places of a head; threads that share a token's place, each a part of the heads
     int rotated_units;                    // vectors of a head that hold pairs (split pairs: of each half)
     float sign;                           // -1: turn back
     double turns[kRotaryMaxPairs];        // frequency of a pair, turns per position
@@ -84,85 +87,81 @@ __device__ __forceinline__ void turn(float& u, float& v, float2 cs) {
 template <typename T, int W, bool INTERLEAVED>
 __global__ void __launch_bounds__(kThreads)
 rotary_kernel(const __grid_constant__ Params p) {
+    constexpr int kAhead = INTERLEAVED ? kHeads : kHeads / 2;
+    constexpr int kAngles = INTERLEAVED ? W / 2 : W;         // of a place (W is 1 only with split pairs)
     extern __shared__ float2 cs[];        // [tokens][pairs]
     const int b = blockIdx.x / p.tiles;
     const int l0 = (int)(blockIdx.x - b * p.tiles) * p.tokens;
     const int tokens = min(p.tokens, p.L - l0);
-    const uint32_t total = (uint32_t)tokens * p.heads_units.d;
-    const T* x = static_cast<const T*>(p.x.data) + (int64_t)b * p.x.batch_stride;
-    T* out = static_cast<T*>(p.out.data) + (int64_t)b * p.out.batch_stride;
+    // this thread's place, token and first head
+    const int slot = (int)divide(threadIdx.x, p.units), unit = (int)threadIdx.x - slot * (int)p.units.d;
+    const int token = (int)divide((uint32_t)slot, p.splits), head0 = slot - token * (int)p.splits.d;
+    const bool live = token < tokens;
+    const bool turned = INTERLEAVED || unit < p.rotated_units;
+    const int col = turned ? unit * W : p.pairs + unit * W;  // first column
+    const T* src = static_cast<const T*>(p.x.data) + (int64_t)b * p.x.batch_stride + (int64_t)(l0 + token) * p.x.token_stride + col;
+    T* dst = static_cast<T*>(p.out.data) + (int64_t)b * p.out.batch_stride + (int64_t)(l0 + token) * p.out.token_stride + col;
+    const int end = live ? p.H : 0;
+    const int step = (int)p.splits.d;
 
-    Vec<T, W> lo[kAhead], hi[kAhead];
-    // vector u of the block: token, head and place in the head; with split
-    // pairs a place holds a vector of each half, or a copied one
-    auto place = [&](uint32_t u, int& token, int& head, int& unit) {
-        token = (int)divide(u, p.heads_units);
-        const uint32_t r = u - (uint32_t)token * p.heads_units.d;
-        head = (int)divide(r, p.units);
-        unit = (int)(r - (uint32_t)head * p.units.d);
-    };
-    auto column = [&](int unit) {         // first column of a vector
-        return INTERLEAVED || unit < p.rotated_units ? unit * W : p.pairs + unit * W;
-    };
-    auto load = [&](uint32_t first) {
+    Vec<T, W> lo[kAhead], hi[INTERLEAVED ? 1 : kAhead];
+    auto load = [&](int head) {
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
-            const uint32_t u = first + i * kThreads;
-            if (u >= total) break;
-            int token, head, unit;
-            place(u, token, head, unit);
-            const T* src = x + (int64_t)(l0 + token) * p.x.token_stride + (int64_t)head * p.x.head_stride + column(unit);
-            lo[i].word = *reinterpret_cast<const decltype(lo[i].word)*>(src);
-            if (!INTERLEAVED && unit < p.rotated_units)
-                hi[i].word = *reinterpret_cast<const decltype(hi[i].word)*>(src + p.pairs);
+            const int h = head + i * step;
+            if (h >= end) break;
+            const T* from = src + (int64_t)h * p.x.head_stride;
+            lo[i].word = *reinterpret_cast<const decltype(lo[i].word)*>(from);
+            if (!INTERLEAVED && turned) hi[i].word = *reinterpret_cast<const decltype(hi[i].word)*>(from + p.pairs);
         }
     };
+    load(head0);
 
-    load(threadIdx.x);
     for (int i = threadIdx.x; i < tokens * p.pairs; i += kThreads) {
-        const int token = i / p.pairs, j = i - token * p.pairs;
-        const int64_t at = (int64_t)b * p.pos_batch_stride + (int64_t)(l0 + token) * p.pos_token_stride + p.axis[j];
+        const int t = i / p.pairs, j = i - t * p.pairs;
+        const int64_t at = (int64_t)b * p.pos_batch_stride + (int64_t)(l0 + t) * p.pos_token_stride + p.axis[j];
         const double position = p.pos_f32 ? (double)static_cast<const float*>(p.positions)[at]
                                           : (double)static_cast<const int32_t*>(p.positions)[at];
-        const double t = position * p.turns[j];
+        const double turns = position * p.turns[j];
         float s, c;
-        sincospif((float)(2.0 * (t - rint(t))), &s, &c);
+        sincospif((float)(2.0 * (turns - rint(turns))), &s, &c);
         cs[i] = make_float2(c, p.sign * s);
     }
     __syncthreads();
 
-    for (uint32_t first = threadIdx.x; first < total; first += kAhead * kThreads) {
-        if (first != threadIdx.x) load(first);
+    float2 angle[kAngles];
+#pragma unroll
+    for (int e = 0; e < kAngles; ++e) {
+        const int j = unit * kAngles + e;
+        angle[e] = live && j < p.pairs ? cs[token * p.pairs + j] : make_float2(1.0f, 0.0f);
+    }
+    for (int head = head0; head < end; head += kAhead * step) {
+        if (head != head0) load(head);
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
-            const uint32_t u = first + i * kThreads;
-            if (u >= total) break;
-            int token, head, unit;
-            place(u, token, head, unit);
-            T* dst = out + (int64_t)(l0 + token) * p.out.token_stride + (int64_t)head * p.out.head_stride + column(unit);
-            const float2* a = cs + token * p.pairs;
+            const int h = head + i * step;
+            if (h >= end) break;
+            T* to = dst + (int64_t)h * p.out.head_stride;
             if (INTERLEAVED) {
 #pragma unroll
-                for (int e = 0; e < W; e += 2) {
-                    const int j = (unit * W + e) >> 1;
-                    if (j < p.pairs) {
-                        float f = to_f32(lo[i].v[e]), g = to_f32(lo[i].v[e + 1]);
-                        turn(f, g, a[j]);
-                        from_f32(f, lo[i].v[e]);
-                        from_f32(g, lo[i].v[e + 1]);
-                    }
+                for (int e = 0; e < kAngles; ++e) {
+                    if (unit * kAngles + e >= p.pairs) break;            // the rest is copied as it is
+                    float f = to_f32(lo[i].v[2 * e]), g = to_f32(lo[i].v[2 * e + 1]);
+                    turn(f, g, angle[e]);
+                    from_f32(f, lo[i].v[2 * e]);
+                    from_f32(g, lo[i].v[2 * e + 1]);
                 }
-            } else if (unit < p.rotated_units) {
+            } else if (turned) {
 #pragma unroll
                 for (int e = 0; e < W; ++e) {
                     float f = to_f32(lo[i].v[e]), g = to_f32(hi[i].v[e]);
-                    turn(f, g, a[unit * W + e]);
+                    turn(f, g, angle[e]);
                     from_f32(f, lo[i].v[e]);
                     from_f32(g, hi[i].v[e]);
                 }
-                *reinterpret_cast<decltype(hi[i].word)*>(dst + p.pairs) = hi[i].word;
+                *reinterpret_cast<decltype(hi[i].word)*>(to + p.pairs) = hi[i].word;
             }
-            *reinterpret_cast<decltype(lo[i].word)*>(dst) = lo[i].word;
+            *reinterpret_cast<decltype(lo[i].word)*>(to) = lo[i].word;
         }
     }
 }
@@ -209,12 +208,22 @@ cudaError_t launch_rotary(const RotaryArgs& a, int num_sms, cudaStream_t stream)
     const int w = a.interleaved ? most : vector_values(a.pairs, a.d - 2 * a.pairs, most);
     const int units = a.interleaved ? (int)a.d / w : (a.pairs + (int)(a.d - 2 * a.pairs)) / w;
     p.rotated_units = a.interleaved ? units : a.pairs / w;
+    // threads that share a token's place: as many as leave each a batch of heads, more (fewer heads, fewer tokens of a
+    // block) while the blocks would not fill the SMs twice
+    const int slots = kThreads / units;
+    int heads = a.interleaved ? kHeads : kHeads / 2;
+    int64_t tokens = 1;
+    int splits = 1;
+    while (true) {
+        splits = (int)((a.H + heads - 1) / heads);
+        if (splits > slots) splits = slots;
+        tokens = slots / splits;
+        if (heads == 1 || a.B * ((a.L + tokens - 1) / tokens) >= 2 * num_sms) break;
+        heads = (heads + 1) / 2;
+    }
+    if (tokens > a.L) tokens = a.L;
     p.units = fast_div((uint32_t)units);
-    p.heads_units = fast_div((uint32_t)(a.H * units));
-    // tokens of a block: 8 vectors a thread, fewer while the blocks would not fill the SMs twice
-    int64_t tokens = (8 * kThreads + a.H * units - 1) / (a.H * units);
-    if (tokens > kMaxTokens) tokens = kMaxTokens;
-    while (tokens > 1 && a.B * ((a.L + tokens - 1) / tokens) < 2 * num_sms) tokens = (tokens + 1) / 2;
+    p.splits = fast_div((uint32_t)splits);
     p.tokens = (int)tokens;
     p.tiles = (int)((a.L + tokens - 1) / tokens);
     const int64_t blocks = a.B * p.tiles;
