@@ -27,7 +27,6 @@ from __future__ import annotations
 
 import ctypes
 import functools
-import math
 import struct
 from dataclasses import dataclass
 
@@ -64,7 +63,7 @@ def _ptr(t) -> int | None:
 def _stream(stream) -> int | None:
     if stream is None:
         # the current stream's handle without building a Stream object (3 us of host time a call)
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -222,7 +221,7 @@ _PACK_HEADS = struct.Struct("Pqqq").pack
 
 def _heads(t) -> bytes:
     """A [batch, tokens, heads, d] CUDA tensor (d contiguous) as nvfp4_heads."""
-    if not t.is_cuda:
+    if t.get_device() < 0:
         raise ValueError("tensor must live on a CUDA device")
     sb, sl, sh, _ = t.stride()
     return _PACK_HEADS(t.data_ptr(), sb, sl, sh)
@@ -548,9 +547,10 @@ def _on_device(*tensors) -> None:
     for t in tensors:
         if t is None:
             continue
-        if t.is_cuda and here is None:
-            here = torch.cuda.current_device()
-        if not t.is_cuda or t.get_device() != here:
+        at = t.get_device()                            # -1 on the CPU
+        if here is None and at >= 0:
+            here = torch._C._cuda_getDevice()
+        if at != here:
             raise ValueError(f"tensor on {t.device}: the call runs on the current CUDA device")
 
 
@@ -568,17 +568,30 @@ def gemv_w4a16(x: torch.Tensor, w: NVFP4Tensor | MXTensor, bias: torch.Tensor | 
     """Y = X W^T (+ bias) for at most NVFP4_GEMV_MAX_ROWS rows: X bf16 [M, K]
     (rows may be strided), W NVFP4 or MX [N, K], bias FP32 [N], Y bf16 or FP32."""
     mx = isinstance(w, MXTensor)
-    _require(x.dtype == torch.bfloat16 and x.dim() == 2 and x.shape[1] == w.k, "x must be bf16 [M, w.k]")
-    _require(x.shape[0] <= NVFP4_GEMV_MAX_ROWS, "at most NVFP4_GEMV_MAX_ROWS rows: gemm_w4a16 takes more")
-    _require(x.stride(1) == 1, "x must be contiguous along k")
-    _require(bias is None or (bias.dtype == torch.float32 and bias.shape == (w.rows,) and bias.is_contiguous()),
-             "bias must be a contiguous FP32 [N]")
+    codes, sf, scale, N, K = w.codes, w.sf, None if mx else w.scale, w.rows, w.k
+    if x.dtype is not torch.bfloat16 or x.dim() != 2 or x.shape[1] != K:
+        raise ValueError("x must be bf16 [M, w.k]")
     M = x.shape[0]
-    y = out if out is not None else torch.empty(M, w.rows, dtype=out_dtype, device=x.device)
-    _require(y.dtype in _DT and y.shape == (M, w.rows) and y.is_contiguous(), "out must be a contiguous bf16 or FP32 [M, N]")
-    _on_device(x, w.codes, w.sf, None if mx else w.scale, bias, y)
-    nvfp4_gemv_w4a16(x, max(x.stride(0), w.k), w.codes, w.sf, None if mx else w.scale,
-                     NVFP4_WEIGHTS_MX if mx else NVFP4_WEIGHTS_NVFP4, bias, M, w.rows, w.k, y, _DT[y.dtype], stream)
+    ld, step = x.stride()
+    if M > NVFP4_GEMV_MAX_ROWS:
+        raise ValueError("at most NVFP4_GEMV_MAX_ROWS rows: gemm_w4a16 takes more")
+    if step != 1:
+        raise ValueError("x must be contiguous along k")
+    if bias is not None and (bias.dtype is not torch.float32 or bias.shape != (N,) or not bias.is_contiguous()):
+        raise ValueError("bias must be a contiguous FP32 [N]")
+    if out is None:
+        y = torch.empty(M, N, dtype=out_dtype, device=x.device)
+    else:
+        y = out
+        _require(y.shape == (M, N) and y.is_contiguous(), "out must be a contiguous bf16 or FP32 [M, N]")
+    y_dtype = _DT.get(y.dtype)
+    if y_dtype is None:
+        raise ValueError("out must be a contiguous bf16 or FP32 [M, N]")
+    _on_device(x, codes, sf, scale, bias, y)
+    check(lib().nvfp4_gemv_w4a16(x.data_ptr(), ld if ld > K else K, codes.data_ptr(), sf.data_ptr(),
+                                 None if mx else scale.data_ptr(), NVFP4_WEIGHTS_MX if mx else NVFP4_WEIGHTS_NVFP4,
+                                 None if bias is None else bias.data_ptr(), M, N, K, y.data_ptr(), y_dtype,
+                                 _stream(stream)), "nvfp4_gemv_w4a16")
     if out is None and stream is not None:
         _used_on(stream, y)
     return y
@@ -586,6 +599,8 @@ def gemv_w4a16(x: torch.Tensor, w: NVFP4Tensor | MXTensor, bias: torch.Tensor | 
 
 def _rows16(t: torch.Tensor) -> torch.Tensor:
     """t with its last axis contiguous and 16-byte steps (a copy where it has not)."""
+    if t.is_contiguous() and t.data_ptr() % 16 == 0 and t.shape[-1] * t.element_size() % 16 == 0:
+        return t
     n = 16 // t.element_size()
     if t.stride(-1) == 1 and t.data_ptr() % 16 == 0 and all(
             s % n == 0 and (s >= t.shape[-1] or (s == 0 and i != 1)) for i, (s, size) in
@@ -603,22 +618,28 @@ def rotary(x: torch.Tensor, positions: torch.Tensor, axes, theta: float = 10000.
     (``interleaved``) or halves of the turned part; ``inverse`` turns back.
     ``out``: any [B, L, H, d] view (for instance of a [B, H, L, d] buffer, whose
     rows quantize() takes), or x itself."""
-    _require(x.dim() == 4 and x.dtype in _DT and x.stride(3) == 1, "x must be bf16 or FP32 [B, L, H, d], d contiguous")
-    B, L, H, d = x.shape
+    dtype = _DT.get(x.dtype)
+    if dtype is None or x.dim() != 4 or x.stride(3) != 1:
+        raise ValueError("x must be bf16 or FP32 [B, L, H, d], d contiguous")
+    B, L, H, d = xs = x.shape
     axes = tuple(axes)
     ps, pt = positions.shape, positions.stride()
     per_sample = len(ps) == 3 and ps[0] > 1
-    _require(positions.dtype in (torch.int32, torch.float32) and len(ps) in (2, 3) and ps[-2] == L
-             and ps[-1] == len(axes) and (len(ps) == 2 or ps[0] in (1, B)),
-             "positions must be int32 or FP32 [L, n_axes] or [B, L, n_axes]")
-    _require(pt[-1] == 1 or len(axes) == 1, "positions must be contiguous along the axes")
-    y = out if out is not None else torch.empty(B, L, H, d, dtype=x.dtype, device=x.device)
-    _require(y.dtype == x.dtype and y.shape == x.shape and y.stride(3) == 1, "out must match x, d contiguous")
+    if not (positions.dtype in (torch.int32, torch.float32) and len(ps) in (2, 3) and ps[-2] == L and ps[-1] == len(axes)
+            and (len(ps) == 2 or ps[0] in (1, B))):
+        raise ValueError("positions must be int32 or FP32 [L, n_axes] or [B, L, n_axes]")
+    if pt[-1] != 1 and len(axes) != 1:
+        raise ValueError("positions must be contiguous along the axes")
+    if out is None:
+        y = torch.empty(B, L, H, d, dtype=x.dtype, device=x.device)
+    else:
+        y = out
+        _require(y.dtype == x.dtype and y.shape == xs and y.stride(3) == 1, "out must match x, d contiguous")
     _on_device(x, positions, y)
     flags = (NVFP4_ROTARY_INTERLEAVED if interleaved else 0) | (NVFP4_ROTARY_INVERSE if inverse else 0)
-    nvfp4_rotary(x, positions, NVFP4_POSITION_I32 if positions.dtype == torch.int32 else NVFP4_POSITION_F32,
-                 pt[0] if per_sample else 0, pt[-2], axes, float(theta), B, L, H, d,
-                 _DT[x.dtype], flags, y, stream)
+    check(lib().nvfp4_rotary(_heads(x), positions.data_ptr(), NVFP4_POSITION_I32 if positions.dtype is torch.int32 else
+                             NVFP4_POSITION_F32, pt[0] if per_sample else 0, pt[-2], _ints(axes), len(axes), float(theta), B, L,
+                             H, d, dtype, flags, _heads(y), _stream(stream)), "nvfp4_rotary")
     if out is None and stream is not None:
         _used_on(stream, y)
     return y
@@ -643,15 +664,16 @@ class RotaryEmbedding(torch.autograd.Function):
 
 
 def _attention_sizes(q, k, v, kv_lens):
-    for t in (q, k, v):
-        if t.dim() != 4 or t.dtype is not torch.bfloat16 or t.stride(3) != 1:
-            raise ValueError("q, k and v must be bf16 [batch, tokens, heads, d], d contiguous")
-    B, Lq, H, d = q.shape
-    Lk, Hkv = k.shape[1], k.shape[2]
-    _require(k.shape == (B, Lk, Hkv, d) and v.shape == k.shape, "k and v must be [B, Lk, Hkv, d] of q's B and d")
-    _require(kv_lens is None or (kv_lens.dtype == torch.int32 and kv_lens.shape == (B,) and kv_lens.is_contiguous()),
-             "kv_lens must be a contiguous int32 [B]")
-    return B, H, Hkv, Lq, Lk, d
+    qs, ks, bf16 = q.shape, k.shape, torch.bfloat16
+    if len(qs) != 4 or len(ks) != 4 or v.shape != ks or ks[0] != qs[0] or ks[3] != qs[3]:
+        raise ValueError("q must be [B, Lq, H, d], k and v [B, Lk, Hkv, d]")
+    if (q.dtype is not bf16 or k.dtype is not bf16 or v.dtype is not bf16 or q.stride(3) != 1 or k.stride(3) != 1 or
+            v.stride(3) != 1):
+        raise ValueError("q, k and v must be bf16, d contiguous")
+    B, Lq, H, d = qs
+    if kv_lens is not None and (kv_lens.dtype is not torch.int32 or kv_lens.shape != (B,) or not kv_lens.is_contiguous()):
+        raise ValueError("kv_lens must be a contiguous int32 [B]")
+    return B, H, ks[2], Lq, ks[1], d
 
 
 def cross_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, kv_lens: torch.Tensor | None = None,
@@ -662,13 +684,18 @@ def cross_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, kv_lens: 
     kv_lens[b] keys of sample b (all of them without kv_lens).  scale defaults
     to 1 / sqrt(d).  Returns bf16 [B, Lq, H, d], and with ``return_lse`` the FP32
     [B, H, Lq] log-sum-exp that cross_attention_backward() takes."""
-    B, H, Hkv, Lq, Lk, d = sizes = _attention_sizes(q, k, v, kv_lens)
-    o = out if out is not None else torch.empty(B, Lq, H, d, dtype=torch.bfloat16, device=q.device)
-    _require(o.dtype == torch.bfloat16 and o.shape == q.shape and o.stride(3) == 1, "out must be a bf16 tensor of q's shape")
+    B, H, Hkv, Lq, Lk, d = _attention_sizes(q, k, v, kv_lens)
+    if out is None:
+        o = torch.empty(B, Lq, H, d, dtype=torch.bfloat16, device=q.device)
+    else:
+        o = out
+        _require(o.dtype == torch.bfloat16 and o.shape == q.shape and o.stride(3) == 1, "out must be a bf16 tensor of q's shape")
     lse = torch.empty(B, H, Lq, dtype=torch.float32, device=q.device) if return_lse else None
     _on_device(q, k, v, kv_lens, o, dev_status)
-    nvfp4_cross_attention(q, k, v, kv_lens, 1.0 / math.sqrt(d) if scale is None else float(scale), *sizes, o, lse,
-                          dev_status, stream)
+    check(lib().nvfp4_cross_attention(_heads(q), _heads(k), _heads(v), None if kv_lens is None else kv_lens.data_ptr(),
+                                      d ** -0.5 if scale is None else float(scale), B, H, Hkv, Lq, Lk, d, _heads(o),
+                                      None if lse is None else lse.data_ptr(), _ptr(dev_status), _stream(stream)),
+          "nvfp4_cross_attention")
     if stream is not None:
         _used_on(stream, *([o] if out is None else []), *([lse] if return_lse else []))
     return (o, lse) if return_lse else o
@@ -680,20 +707,28 @@ def cross_attention_backward(grad_out: torch.Tensor, q: torch.Tensor, k: torch.T
                              stream=None):
     """(dq, dk, dv) of cross_attention() from its ``out`` and ``lse``."""
     B, H, Hkv, Lq, Lk, d = sizes = _attention_sizes(q, k, v, kv_lens)
-    for t in (grad_out, out):
-        _require(t.dtype == torch.bfloat16 and t.shape == q.shape and t.stride(3) == 1,
-                 "grad_out and out must be bf16 tensors of q's shape, d contiguous")
-    _require(lse.dtype == torch.float32 and lse.shape == (B, H, Lq) and lse.is_contiguous(),
-             "lse must be a contiguous FP32 [B, H, Lq]")
-    need = nvfp4_cross_attention_backward_workspace_bytes(*sizes)
-    ws = workspace if workspace is not None else torch.empty(need, dtype=torch.uint8, device=q.device)
-    _require(ws.is_contiguous(), "workspace must be contiguous")
-    dq = torch.empty(B, Lq, H, d, dtype=torch.bfloat16, device=q.device)
-    dk, dv = (torch.empty(B, Lk, Hkv, d, dtype=torch.bfloat16, device=q.device) for _ in range(2))
+    shape, bf16, device = q.shape, torch.bfloat16, q.device
+    if (grad_out.dtype is not bf16 or out.dtype is not bf16 or grad_out.shape != shape or out.shape != shape or
+            grad_out.stride(3) != 1 or out.stride(3) != 1):
+        raise ValueError("grad_out and out must be bf16 tensors of q's shape, d contiguous")
+    if lse.dtype is not torch.float32 or lse.shape != (B, H, Lq) or not lse.is_contiguous():
+        raise ValueError("lse must be a contiguous FP32 [B, H, Lq]")
+    if workspace is None:
+        bytes_ = nvfp4_cross_attention_backward_workspace_bytes(*sizes)
+        ws = torch.empty(bytes_, dtype=torch.uint8, device=device)
+    else:
+        ws = workspace
+        _require(ws.is_contiguous(), "workspace must be contiguous")
+        bytes_ = ws.numel() * ws.element_size()
+    dq = torch.empty(B, Lq, H, d, dtype=bf16, device=device)
+    dk = torch.empty(B, Lk, Hkv, d, dtype=bf16, device=device)
+    dv = torch.empty(B, Lk, Hkv, d, dtype=bf16, device=device)
     _on_device(grad_out, q, k, v, out, lse, kv_lens, ws, dev_status)
-    nvfp4_cross_attention_backward(grad_out, q, k, v, out, lse, kv_lens, 1.0 / math.sqrt(d) if scale is None else
-                                   float(scale), *sizes, dq, dk, dv, ws, ws.numel() * ws.element_size(), dev_status,
-                                   stream)
+    check(lib().nvfp4_cross_attention_backward(
+        _heads(grad_out), _heads(q), _heads(k), _heads(v), _heads(out), lse.data_ptr(),
+        None if kv_lens is None else kv_lens.data_ptr(), d ** -0.5 if scale is None else float(scale), B, H, Hkv, Lq, Lk, d,
+        _heads(dq), _heads(dk), _heads(dv), ws.data_ptr(), bytes_, _ptr(dev_status), _stream(stream)),
+        "nvfp4_cross_attention_backward")
     if stream is not None:
         _used_on(stream, dq, dk, dv, *((ws,) if workspace is None else ()))
     return dq, dk, dv

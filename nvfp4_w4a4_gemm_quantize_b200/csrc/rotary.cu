@@ -196,12 +196,18 @@ cudaError_t launch_rotary(const RotaryArgs& a, int num_sms, cudaStream_t stream)
     p.H = (int)a.H;
     p.pairs = a.pairs;
     p.sign = a.inverse ? -1.0f : 1.0f;
+    // theta^(-k / n) as a product of two powers, so that 32 pairs take 11 calls instead of 32 (64-bit: two roundings more)
     int j = 0;
-    for (int i = 0; i < a.n_axes; ++i)
-        for (int k = 0; k < a.axis_pairs[i]; ++k, ++j) {
-            p.turns[j] = std::pow(a.theta, -(double)k / a.axis_pairs[i]) / 6.283185307179586476925287;
+    for (int i = 0; i < a.n_axes; ++i) {
+        const int n = a.axis_pairs[i];
+        double low[8], high = 1.0;
+        for (int k = 0; k < n; ++k, ++j) {
+            if (k < 8) low[k] = std::pow(a.theta, -(double)k / n) / 6.283185307179586476925287;
+            if (k % 8 == 0) high = k == 0 ? 1.0 : std::pow(a.theta, -(double)k / n);
+            p.turns[j] = low[k % 8] * high;
             p.axis[j] = (uint8_t)i;
         }
+    }
     const int most = a.f32 ? 4 : 8;
     // interleaved pairs: d % 8 == 0, so full vectors; split pairs: a vector
     // must not straddle the halves or the copied tail
