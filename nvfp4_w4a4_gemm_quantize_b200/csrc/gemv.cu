@@ -10,7 +10,7 @@
 // one 16-byte word of the scale layout for each lane.  A lane reads 16 code bytes
 // a feature, 32 neighbouring k: the order of k within a product is free as long as
 // x comes in the same one, so nothing is shuffled.
-// Work: a cluster of 1 to 8 blocks of 12 or 16 warps takes a range of the 32-feature
+// Work: a cluster of 1 to 8 blocks of 16 warps takes a range of the 32-feature
 // units; its blocks split k (each keeps its part of x in shared memory), a block's
 // warps split the block's items evenly, in order.  Sums are joined in a fixed order
 // (warps, then blocks over distributed shared memory): results do not depend on
@@ -36,9 +36,8 @@
 namespace nvfp4 {
 namespace gemv {
 
-// Warps of a block: as many as leave a thread the registers it needs (128, 168).
-template <int NT, bool MX>
-constexpr int kWarpsOf = NT == 1 && !MX ? 16 : 12;
+constexpr int kThreads = 512;
+constexpr int kWarps = kThreads / 32;
 constexpr int kStepK = 128;                   // k of an item
 constexpr int kUnitN = 32;                    // features of an item
 constexpr int kMaxCluster = 8;
@@ -59,17 +58,34 @@ struct Item {
     uint4 codes[4];
     uint4 sf;                                 // word i: four blocks of feature i
 };
+constexpr int kItemBytes = 5 * 512;           // of a warp
 
-__device__ __forceinline__ uint4 load_stream(const void* p) {
-    uint4 r;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
-    return r;
+// Items a warp has in shared memory, the current one and those on their way (asynchronous copies: with the next two in
+// registers there was room for 12 warps, and x waited for the weights behind it): as many as leave x its room.
+template <int NT>
+constexpr int kDepth = NT == 1 ? 4 : 2;
+template <int NT>
+constexpr int kXBytes = NT == 1 ? 36 * 1024 : 96 * 1024;
+
+// 16 bytes to shared memory, zeros where !valid.
+__device__ __forceinline__ void copy_async(uint32_t dst, const void* src, bool valid) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 __device__ __forceinline__ uint4 load_cached(const void* p) {
     uint4 r;
     asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
+    return r;
+}
+
+__device__ __forceinline__ uint4 load_shared(uint32_t at) {
+    uint4 r;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(at) : "memory");
     return r;
 }
 
@@ -298,13 +314,12 @@ __device__ __noinline__ void item_bf16(const Item* from, const uint8_t* const* x
 }
 
 template <int NT, bool MX>
-__global__ void __launch_bounds__(32 * kWarpsOf<NT, MX>, 1) gemv_kernel(const Params p) {
-    constexpr int kWarps = kWarpsOf<NT, MX>, kThreads = 32 * kWarps;
-    constexpr int kAhead = NT == 2 && MX ? 1 : 2;           // items on their way while one is computed, as registers allow
+__global__ void __launch_bounds__(kThreads, 1) gemv_kernel(const Params p) {
+    constexpr int kAhead = kDepth<NT>;
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ uint32_t x_max[16], x_min[16];               // of a row's k range: largest |x|, smallest nonzero |x| - 1, as bits
     __shared__ int head_unit[kWarps];                       // the unit a warp starts inside of, or -1
-    constexpr int kEarly = NT == 1 ? 2 : 1;                             // pieces of x a thread loads before the first weights
+    constexpr int kEarly = 2;                               // pieces of x a thread loads before the first weights
 
     const GemvArgs& a = p.a;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -313,8 +328,9 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT, MX>, 1) gemv_kernel(const Pa
     const int u_first = c * p.units_each + min(c, p.units_more), u_last = u_first + p.units_each + (c < p.units_more ? 1 : 0);
     const int k_first = rank * p.steps_each + min(rank, p.steps_more), k_last = k_first + p.steps_each + (rank < p.steps_more ? 1 : 0);
     const int row_bytes = p.segment * 256 + 64;
-    uint8_t* const xs = smem;                               // [M][segment][4][4] 16-byte pieces of x (+ 64 bytes a row)
-    float* const part = reinterpret_cast<float*>(smem + a.M * row_bytes);      // [unit_chunk][M][32]: sums
+    const uint32_t ring = smem_u32(smem) + (threadIdx.x >> 5) * kAhead * kItemBytes + (threadIdx.x & 31) * 16;   // [slot][5][lane]
+    uint8_t* const xs = smem + kWarps * kAhead * kItemBytes;    // [M][segment][4][4] 16-byte pieces of x (+ 64 bytes a row)
+    float* const part = reinterpret_cast<float*>(xs + a.M * row_bytes);      // [unit_chunk][M][32]: sums
     float* const heads = part + p.unit_chunk * kUnitN * a.M;                   // [warp][M][32]: sums of units begun by another warp
     const int unit_floats = kUnitN * a.M;
     const int64_t row_codes = a.K / 2;
@@ -343,15 +359,21 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT, MX>, 1) gemv_kernel(const Pa
                 codes = a.w_codes + (int64_t)n * row_codes + 16 * t;
                 sf = a.w_sf + (int64_t)(u >> 2) * p.kb4 * 512 + ((u & 3) * 8 + g) * 16;
             };
-            auto fetch = [&](Item& it) {
-                if (left <= 0) return;
+            auto fetch = [&](int slot) {
+                if (left <= 0) {
+                    copies_commit();
+                    return;
+                }
                 const int s = k0 + fk;
                 const bool in = s * kStepK + 32 * t < a.K;  // a last half step has no k for t >= 2
+                const uint32_t dst = ring + slot * kItemBytes;
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    it.codes[i] = in && (have >> i & 1u) ? load_stream(codes + i * 32 * row_codes + (int64_t)s * 64)
-                                                         : make_uint4(0, 0, 0, 0);
-                it.sf = in ? load_stream(sf + (int64_t)(MX ? s : 2 * s + (t >> 1)) * 512) : make_uint4(0, 0, 0, 0);
+                for (int i = 0; i < 4; ++i) {
+                    const bool valid = in && (have >> i & 1u);
+                    copy_async(dst + i * 512, valid ? codes + i * 32 * row_codes + (int64_t)s * 64 : a.w_codes, valid);
+                }
+                copy_async(dst + 4 * 512, in ? sf + (int64_t)(MX ? s : 2 * s + (t >> 1)) * 512 : a.w_sf, in);
+                copies_commit();
                 --left;
                 if (++fk == steps) {
                     fk = 0;
@@ -375,10 +397,9 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT, MX>, 1) gemv_kernel(const Pa
             for (int i = 0; i < kEarly; ++i) early[i] = m_first < a.M ? load_x(m_first, p_first + i * p_step) : make_uint4(0, 0, 0, 0);
             int unit = fu, step = fk;
             const bool begins = fk == 0, some = item < end;
-            Item queue[kAhead + 1];
             if (left > 0) aim();
 #pragma unroll
-            for (int i = 0; i < kAhead; ++i) fetch(queue[i]);
+            for (int i = 0; i < kAhead; ++i) fetch(i);
 
             if (u0 != u_first || k0 != k_first) __syncthreads();
             if (threadIdx.x < 16) {
@@ -523,13 +544,16 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT, MX>, 1) gemv_kernel(const Pa
                     ++unit;
                 }
             };
-            while (item < end) {
+            for (int slot = 0; item < end; slot = slot + 1 == kAhead ? 0 : slot + 1) {
+                copies_wait<kAhead - 1>();                  // a lane reads what it copied itself
+                Item it;
 #pragma unroll
-                for (int i = 0; i <= kAhead; ++i) {
-                    fetch(queue[(i + kAhead) % (kAhead + 1)]);
-                    if (item < end) run(queue[i]);
-                }
+                for (int i = 0; i < 4; ++i) it.codes[i] = load_shared(ring + slot * kItemBytes + i * 512);
+                it.sf = load_shared(ring + slot * kItemBytes + 4 * 512);
+                run(it);
+                fetch(slot);
             }
+            copies_wait<0>();
             if (some && step != 0) flush();
             __syncthreads();
             // what warps added to units that another one began, in the warps' order; a warp takes every kWarps-th unit
@@ -576,7 +600,7 @@ cudaError_t launch(const Params& p, int clusters, int ranks, int smem, cudaStrea
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)clusters, (unsigned)ranks);
-    cfg.blockDim = dim3(32 * kWarpsOf<NT, MX>);
+    cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = (size_t)smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr;
@@ -605,7 +629,7 @@ int64_t resident_clusters(bool two, bool mx, int ranks, int num_sms) {
         if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit) != cudaSuccess) return 1;
         cudaLaunchConfig_t cfg{};
         cfg.gridDim = dim3((unsigned)num_sms, (unsigned)ranks);
-        cfg.blockDim = dim3(!two && !mx ? 32 * kWarpsOf<1, false> : 32 * kWarpsOf<2, true>);
+        cfg.blockDim = dim3(kThreads);
         cfg.dynamicSmemBytes = kSmemLimit;
         cudaLaunchAttribute attr;
         attr.id = cudaLaunchAttributeClusterDimension;
@@ -634,14 +658,13 @@ cudaError_t launch_gemv(const GemvArgs& a, int num_sms, cudaStream_t stream) {
     p.kb4 = a.K / (a.mx ? 128 : 64);
     // Blocks along k: the number that ends first, in items of a warp; a cluster's start and join cost about two, a block
     // reads its part of x first.  The clusters all run at once: more of them than the GPCs hold would double the time.
-    const int warps = a.M <= 8 && !a.mx ? kWarpsOf<1, false> : kWarpsOf<2, true>;
     int ranks = 1, clusters = 1;
     int64_t best = 0;
     for (int r = 1; r <= kMaxCluster && r <= p.steps; r *= 2) {
         const int64_t most = resident_clusters(a.M > 8, a.mx, r, num_sms);
         const int64_t c = p.units < most ? p.units : most;
         const int64_t per = (p.units + c - 1) / c, steps = (p.steps + r - 1) / r;
-        const int64_t cost = 16 * ((per * steps + warps - 1) / warps + (r > 1 ? 2 : 0)) + a.M * steps / 9;
+        const int64_t cost = 16 * ((per * steps + kWarps - 1) / kWarps + (r > 1 ? 2 : 0)) + a.M * steps / 9;
         if (best == 0 || cost < best) {
             best = cost;
             ranks = r;
@@ -654,14 +677,15 @@ cudaError_t launch_gemv(const GemvArgs& a, int num_sms, cudaStream_t stream) {
     p.steps_more = p.steps % ranks;
     const int steps = (p.steps + ranks - 1) / ranks;
     const int unit_bytes = kUnitN * a.M * 4;
-    // shared memory: x of a k segment (at most 96 KB), the warps' heads, the sums of as many units as are left room for
-    p.segment = (96 * 1024 / a.M - 64) / 256;
+    // shared memory: the warps' items, x of a k segment, the warps' heads, the sums of as many units as are left room for
+    const int ring_bytes = kWarps * kItemBytes * (a.M <= 8 ? kDepth<1> : kDepth<2>);
+    p.segment = ((a.M <= 8 ? kXBytes<1> : kXBytes<2>) / a.M - 64) / 256;
     if (p.segment > steps) p.segment = steps;
     const int x_bytes = a.M * (p.segment * 256 + 64);
     const int per = (p.units + clusters - 1) / clusters;
-    p.unit_chunk = (kSmemLimit - x_bytes - warps * unit_bytes) / unit_bytes;
+    p.unit_chunk = (kSmemLimit - ring_bytes - x_bytes - kWarps * unit_bytes) / unit_bytes;
     if (p.unit_chunk > per) p.unit_chunk = per;
-    const int smem = x_bytes + (warps + p.unit_chunk) * unit_bytes;
+    const int smem = ring_bytes + x_bytes + (kWarps + p.unit_chunk) * unit_bytes;
     if (a.M <= 8)
         return a.mx ? launch<1, true>(p, clusters, ranks, smem, stream) : launch<1, false>(p, clusters, ranks, smem, stream);
     return a.mx ? launch<2, true>(p, clusters, ranks, smem, stream) : launch<2, false>(p, clusters, ranks, smem, stream);
