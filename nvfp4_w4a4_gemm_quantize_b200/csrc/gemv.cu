@@ -89,6 +89,12 @@ __device__ __forceinline__ uint4 load_shared(uint32_t at) {
     return r;
 }
 
+__device__ __forceinline__ uint32_t load_shared_word(uint32_t at) {
+    uint32_t r;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(r) : "r"(at) : "memory");
+    return r;
+}
+
 // E2M1 codes p and p + 4 of a word (pair p = 0 .. 3) as bf16 times 2^-126: the
 // sign to bit 15, exponent and mantissa to bits 6-8, where bf16's two lowest
 // exponent values read E2M1's, zero and its subnormal included.  One product
@@ -181,7 +187,7 @@ __device__ __forceinline__ void item_f16_nvfp4(const Item& it, const uint8_t* co
     for (int w = 0; w < 4; ++w) {
         uint4 b[NT];
 #pragma unroll
-        for (int j = 0; j < NT; ++j) b[j] = *reinterpret_cast<const uint4*>(xrow[j] + w * 64);
+        for (int j = 0; j < NT; ++j) b[j] = *reinterpret_cast<const uint4*>(xrow[j] + w * 64 + t * 16);
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
             uint32_t f[2][4];
@@ -201,73 +207,86 @@ __device__ __forceinline__ void item_f16_nvfp4(const Item& it, const uint8_t* co
     }
 }
 
-// MX: weights times 2^(their scale's byte - the item's largest, of the feature), the sums times 2^(that - 128).  Lanes
-// of a column share no block, so a lane has one scale a feature.  Where a block is more than 2^23 below the largest
-// (E2M1 would leave FP16), the item runs once per block, the others' codes as zeros.
-template <int NT, bool WIDE>
-__device__ __forceinline__ void item_f16_mx(const Item& it, const uint8_t* const (&xrow)[NT], int t, const uint32_t (&top)[4],
-                                            const uint32_t (&mine)[4], const float (&undo)[NT][2], float (&acc)[2][NT][4]) {
-#pragma unroll 1
-    for (int only = WIDE ? 0 : 4; only < (WIDE ? 4 : 5); ++only) {
-        uint32_t sc[4];
-        float whole[4];
+// One item of one row in FP16, NVFP4: the eight columns of B hold the row's eight blocks, each lane column's 32 k its
+// two (zeros elsewhere), so a product's sums come apart by block and the scales are applied to them in FP32.
+__device__ __forceinline__ void item_f16_one(const Item& it, const uint8_t* xrow, int g, int t, float (&acc)[4]) {
+    float sum[2][4] = {};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t at = only < 4 ? (word_of(it.sf, i) >> (8 * only)) & 0xFFu : top[i];
-            const uint32_t down = only < 4 ? 0u : top[i] - mine[i];            // FP16 2^-down, subnormal past 14
-            const uint32_t h = __half_as_ushort(__float2half_rn(__uint_as_float((127u - down) << 23)));
-            sc[i] = only < 4 && only != t ? 0u : h * 0x10001u;
-            whole[i] = __uint_as_float(at > 1u ? (at - 1u) << 23 : 0x00200000u << at);      // 2^(at - 128)
+    for (int w = 0; w < 4; ++w) {
+        uint4 b = make_uint4(0, 0, 0, 0);
+        if (g == t + 4 * (w >> 1)) b = *reinterpret_cast<const uint4*>(xrow + w * 64 + t * 16);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            uint32_t f[2][4];
+            decode_f16(word_of(it.codes[2 * u], w), f[0]);
+            decode_f16(word_of(it.codes[2 * u + 1], w), f[1]);
+            mma<true>(sum[u], f[0][0], f[1][0], f[0][1], f[1][1], b.x, b.y);
+            mma<true>(sum[u], f[0][2], f[1][2], f[0][3], f[1][3], b.z, b.w);
         }
-        float sum[2][NT][4] = {};
+    }
+    // columns 2 t and 2 t + 1: blocks 0 2, 4 6, 1 3, 5 7 (the lane's scale words are of the atom with its two)
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-            uint4 b[NT];
-#pragma unroll
-            for (int j = 0; j < NT; ++j) b[j] = *reinterpret_cast<const uint4*>(xrow[j] + w * 64);
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                uint32_t f[2][4];
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    decode_f16(word_of(it.codes[2 * u + i], w), f[i]);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) f[i][e] = mul_f16x2(f[i][e], sc[2 * u + i]);
-                }
-#pragma unroll
-                for (int half = 0; half < 2; ++half)
-#pragma unroll
-                    for (int j = 0; j < NT; ++j)
-                        mma<true>(sum[u][j], f[0][2 * half], f[1][2 * half], f[0][2 * half + 1], f[1][2 * half + 1], half ? b[j].z : b[j].x,
-                                  half ? b[j].w : b[j].y);
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-            for (int j = 0; j < NT; ++j)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    acc[u][j][e] = fmaf(sum[u][j][e] * undo[j][e & 1], whole[2 * u + (e >> 1)], acc[u][j][e]);
+    for (int i = 0; i < 4; ++i) {
+        uint32_t h;
+        const uint16_t two = (uint16_t)(__byte_perm(word_of(it.sf, i), 0, t < 2 ? 0x4420 : 0x4431) & 0x7F7Fu);
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(two));
+        const float2 s = __half22float2(*reinterpret_cast<const __half2*>(&h));
+        acc[i] = fmaf(sum[i >> 1][2 * (i & 1)], s.x, acc[i]);
+        acc[i] = fmaf(sum[i >> 1][2 * (i & 1) + 1], s.y, acc[i]);
     }
 }
 
-// The item of a wide spread, out of line: nothing of it stays in registers where it is not called.
-template <int NT>
-__device__ __noinline__ void item_f16_mx_wide(const Item* it, const uint8_t* const* xrow, int t, const float* back, float* acc) {
-    const uint32_t none[4] = {0, 0, 0, 0};
-    float undo[NT][2];
+// One item in FP16, MX: a block's 32 k are one 16-byte piece of a feature, of which lane t takes word t, so that a
+// product's sums are of one block and its scale is applied to them in FP32, times 2^(byte - 128).  Pieces lie in the
+// order the copies gave them: (4 g + (block ^ (g / 2 & 3))) 16 bytes into the feature's 512.
+// SAFE: the rows' powers of two are undone first (see below).
+template <int NT, bool SAFE>
+__device__ __forceinline__ void item_f16_mx(uint32_t item, const uint4& sf, const uint8_t* const (&xrow)[NT], int g, int t,
+                                            const float (&undo)[NT][2], float (&acc)[2][NT][4]) {
 #pragma unroll
-    for (int i = 0; i < 2 * NT; ++i) (&undo[0][0])[i] = back[i];
+    for (int c = 0; c < 4; ++c) {
+        uint4 b[NT];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) b[j] = *reinterpret_cast<const uint4*>(xrow[j] + c * 64 + t * 16);
+        const uint32_t at = item + (4 * g + (c ^ ((g >> 1) & 3))) * 16 + 4 * t;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            uint32_t f[2][4];
+            float s[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                decode_f16(load_shared_word(at + (2 * u + i) * 512), f[i]);
+                const uint32_t e = (word_of(sf, 2 * u + i) >> (8 * c)) & 0xFFu;
+                s[i] = __uint_as_float(e > 1u ? (e - 1u) << 23 : 0x00200000u << e);
+            }
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                float sum[4] = {};
+                mma<true>(sum, f[0][0], f[1][0], f[0][1], f[1][1], b[j].x, b[j].y);
+                mma<true>(sum, f[0][2], f[1][2], f[0][3], f[1][3], b[j].z, b[j].w);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    acc[u][j][e] = fmaf(SAFE ? sum[e] * undo[j][e & 1] : sum[e], s[e >> 1], acc[u][j][e]);
+            }
+        }
+    }
+}
+
+// Out of line: nothing of it stays in registers where it is not called.
+template <int NT>
+__device__ __noinline__ void item_f16_mx_safe(uint32_t item, const uint4* sf, const uint8_t* const* xrow, int g, int t,
+                                              const float* back, float* sums) {
     const uint8_t* xr[NT];
-    float sum[2][NT][4];
+    float undo[NT][2], acc[2][NT][4];
 #pragma unroll
     for (int j = 0; j < NT; ++j) xr[j] = xrow[j];
 #pragma unroll
-    for (int i = 0; i < 8 * NT; ++i) (&sum[0][0][0])[i] = acc[i];
-    item_f16_mx<NT, true>(*it, xr, t, none, none, undo, sum);
+    for (int i = 0; i < 2 * NT; ++i) (&undo[0][0])[i] = back[i];
 #pragma unroll
-    for (int i = 0; i < 8 * NT; ++i) acc[i] = (&sum[0][0][0])[i];
+    for (int i = 0; i < 8 * NT; ++i) (&acc[0][0][0])[i] = sums[i];
+    item_f16_mx<NT, true>(item, *sf, xr, g, t, undo, acc);
+#pragma unroll
+    for (int i = 0; i < 8 * NT; ++i) sums[i] = (&acc[0][0][0])[i];
 }
 
 // One item in bf16: x pairs in the order (0,4) (1,5) (2,6) (3,7) of a code word.
@@ -286,7 +305,7 @@ __device__ __noinline__ void item_bf16(const Item* from, const uint8_t* const* x
     for (int w = 0; w < 4; ++w) {
         uint4 b[NT];
 #pragma unroll
-        for (int j = 0; j < NT; ++j) b[j] = *reinterpret_cast<const uint4*>(xrow[j] + w * 64);
+        for (int j = 0; j < NT; ++j) b[j] = *reinterpret_cast<const uint4*>(xrow[j] + (MX ? t * 64 + w * 16 : w * 64 + t * 16));
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
             uint32_t f[4][2];
@@ -313,7 +332,8 @@ __device__ __noinline__ void item_bf16(const Item* from, const uint8_t* const* x
     for (int i = 0; i < 8 * NT; ++i) sums[i] = (&acc[0][0][0])[i];
 }
 
-template <int NT, bool MX>
+// ONE: a single row.
+template <int NT, bool MX, bool ONE>
 __global__ void __launch_bounds__(kThreads, 1) gemv_kernel(const Params p) {
     constexpr int kAhead = kDepth<NT>;
     extern __shared__ __align__(16) uint8_t smem[];
@@ -328,7 +348,9 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_kernel(const Params p) {
     const int u_first = c * p.units_each + min(c, p.units_more), u_last = u_first + p.units_each + (c < p.units_more ? 1 : 0);
     const int k_first = rank * p.steps_each + min(rank, p.steps_more), k_last = k_first + p.steps_each + (rank < p.steps_more ? 1 : 0);
     const int row_bytes = p.segment * 256 + 64;
-    const uint32_t ring = smem_u32(smem) + (threadIdx.x >> 5) * kAhead * kItemBytes + (threadIdx.x & 31) * 16;   // [slot][5][lane]
+    // this warp's items [slot][5][32] of 16 bytes, and this lane's place in them (MX: swizzled, see item_f16_mx)
+    const uint32_t items = smem_u32(smem) + warp * kAhead * kItemBytes;
+    const uint32_t ring = items + (MX ? 4 * g + (t ^ ((g >> 1) & 3)) : lane) * 16;
     uint8_t* const xs = smem + kWarps * kAhead * kItemBytes;    // [M][segment][4][4] 16-byte pieces of x (+ 64 bytes a row)
     float* const part = reinterpret_cast<float*>(xs + a.M * row_bytes);      // [unit_chunk][M][32]: sums
     float* const heads = part + p.unit_chunk * kUnitN * a.M;                   // [warp][M][32]: sums of units begun by another warp
@@ -337,7 +359,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_kernel(const Params p) {
 
     const uint8_t* xrow[NT];
 #pragma unroll
-    for (int j = 0; j < NT; ++j) xrow[j] = xs + min(8 * j + g, a.M - 1) * row_bytes + t * 16;
+    for (int j = 0; j < NT; ++j) xrow[j] = xs + (ONE ? 0 : min(8 * j + g, a.M - 1)) * row_bytes;
 
     for (int u0 = u_first; u0 < u_last; u0 += p.unit_chunk) {
         const int units = min(p.unit_chunk, u_last - u0);
@@ -372,7 +394,10 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_kernel(const Params p) {
                     const bool valid = in && (have >> i & 1u);
                     copy_async(dst + i * 512, valid ? codes + i * 32 * row_codes + (int64_t)s * 64 : a.w_codes, valid);
                 }
-                copy_async(dst + 4 * 512, in ? sf + (int64_t)(MX ? s : 2 * s + (t >> 1)) * 512 : a.w_sf, in);
+                // scales: of the lane's own blocks, or (ONE) of the atom with its columns' blocks
+                const int atom = MX ? s : 2 * s + (ONE ? t & 1 : t >> 1);
+                const bool has = atom < p.kb4;
+                copy_async(dst + 4 * 512, has ? sf + (int64_t)atom * 512 : a.w_sf, has);
                 copies_commit();
                 --left;
                 if (++fk == steps) {
@@ -386,7 +411,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_kernel(const Params p) {
             const int p_first = (warp % per_row) * 32 + lane, p_step = per_row * 32;
             const int m_first = warp / per_row, m_step = kWarps / per_row;
             auto piece = [&](int m, int q) {
-                return reinterpret_cast<uint4*>(xs + m * row_bytes + (q >> 4) * 256 + (q & 3) * 64 + ((q >> 2) & 3) * 16);
+                return reinterpret_cast<uint4*>(xs + m * row_bytes + (q >> 4) * 256 + (MX ? (q & 15) * 16 : (q & 3) * 64 + ((q >> 2) & 3) * 16));
             };
             auto load_x = [&](int m, int q) {
                 const int k = k0 * kStepK + q * 8;
@@ -444,7 +469,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_kernel(const Params p) {
             bool fits = true;                               // every row within FP16's exact range
             for (int i = 0; i < a.M; ++i) {
                 const int top = (int)(x_max[i] >> 7), low = (int)((x_min[i] + 1) >> 7);
-                fits = fits && (x_max[i] == 0 || (top >= 64 && top <= 190 && low >= top - 31));
+                fits = fits && (x_max[i] == 0 || (top >= 64 && top <= (MX ? 141 : 190) && low >= top - 31));
             }
             for (int m = m_first; m < a.M; m += m_step) {
                 const int top = (int)(x_max[m] >> 7);
@@ -476,12 +501,21 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_kernel(const Params p) {
                 const uint32_t top = x_max[8 * (i >> 1) + 2 * t + (i & 1)] >> 7;
                 undo[i >> 1][i & 1] = fits && top ? __uint_as_float((top - 14u) << 23) : 1.0f;
             }
-            float acc[2][NT][4] = {};
-            bool first_unit = true;
+            float acc[2][NT][4] = {}, one[4] = {};
+            bool first_unit = true, raised = false;
             auto flush = [&]() {                            // sums of the unit, in units of x and the weights
                 const bool head = first_unit && !begins;
                 float* dst = head ? heads + warp * unit_floats : part + unit * unit_floats;
                 const bool add = !head && k0 != k_first;
+                if (ONE && fits) {                          // a lane's columns are blocks: their sum is the row's
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        one[i] += __shfl_xor_sync(0xffffffffu, one[i], 1);
+                        one[i] += __shfl_xor_sync(0xffffffffu, one[i], 2);
+                        acc[i >> 1][0][2 * (i & 1)] = one[i];
+                        one[i] = 0.0f;
+                    }
+                }
 #pragma unroll
                 for (int j = 0; j < NT; ++j)
 #pragma unroll
@@ -489,7 +523,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_kernel(const Params p) {
                         const int row = 8 * j + 2 * t + c;
                         if (row >= a.M) continue;
                         // the bf16 path's NVFP4 weights are 2^-7 of theirs, the FP16 path's E8M0 scales half of theirs
-                        const float by = fits ? (MX ? 2.0f : undo[j][c]) : (MX ? 1.0f : 128.0f);
+                        const float by = fits ? (MX ? (raised ? 2.0f : 2.0f * undo[j][c]) : undo[j][c]) : (MX ? 1.0f : 128.0f);
 #pragma unroll
                         for (int u = 0; u < 2; ++u)
 #pragma unroll
@@ -501,39 +535,45 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_kernel(const Params p) {
                             }
                     }
                 first_unit = false;
+                raised = false;
             };
-            auto run = [&](Item& it) {
+            auto run = [&](Item& it, uint32_t at) {
                 const uint8_t* xr[NT];
 #pragma unroll
                 for (int j = 0; j < NT; ++j) xr[j] = xrow[j] + step * 256;
-                uint32_t top[4], mine[4];
-                bool wide = false;
-                if (MX) {
+                if (MX && fits && !raised) {
+                    // Scales above 2^90 could leave FP32's range with the rows' powers of two: from such an item on, the
+                    // unit's sums are kept without them.
+                    const uint32_t m = __vmaxu4(__vmaxu4(it.sf.x, it.sf.y), __vmaxu4(it.sf.z, it.sf.w));
+                    raised = __any_sync(0xffffffffu, __vcmpgtu4(m, 0xD9D9D9D9u) != 0u);
+                    if (raised)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint32_t s = word_of(it.sf, i), m = __vmaxu4(s, s >> 16);
-                        mine[i] = (s >> (8 * t)) & 0xFFu;
-                        top[i] = max(m & 0xFFu, (m >> 8) & 0xFFu);
-                        wide = wide || top[i] - mine[i] > 23u;
-                    }
-                    wide = __any_sync(0xffffffffu, wide);
+                        for (int u = 0; u < 2; ++u)
+#pragma unroll
+                            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) acc[u][j][e] *= undo[j][e & 1];
                 }
-                if (!fits || wide) {
-                    const Item copy = it;
-                    float sums[8 * NT];
+                if (!fits || raised) {
+                    Item copy = it;
+                    if (ONE) {                              // the scales of the lane's own blocks, from a lane that has them
+                        const int from = (lane & ~3) | (t >> 1);
+                        copy.sf = make_uint4(__shfl_sync(0xffffffffu, it.sf.x, from), __shfl_sync(0xffffffffu, it.sf.y, from),
+                                             __shfl_sync(0xffffffffu, it.sf.z, from), __shfl_sync(0xffffffffu, it.sf.w, from));
+                    }
+                    float sums[8 * NT], back[2 * NT];
 #pragma unroll
                     for (int i = 0; i < 8 * NT; ++i) sums[i] = (&acc[0][0][0])[i];
-                    if (!fits) item_bf16<NT, MX>(&copy, xr, t, sums);
-                    else {
-                        float back[2 * NT];
 #pragma unroll
-                        for (int i = 0; i < 2 * NT; ++i) back[i] = (&undo[0][0])[i];
-                        item_f16_mx_wide<NT>(&copy, xr, t, back, sums);
-                    }
+                    for (int i = 0; i < 2 * NT; ++i) back[i] = (&undo[0][0])[i];
+                    if (!fits) item_bf16<NT, MX>(&copy, xr, t, sums);
+                    else if (MX) item_f16_mx_safe<NT>(at, &copy.sf, xr, g, t, back, sums);
 #pragma unroll
                     for (int i = 0; i < 8 * NT; ++i) (&acc[0][0][0])[i] = sums[i];
                 } else if (MX) {
-                    item_f16_mx<NT, false>(it, xr, t, top, mine, undo, acc);
+                    item_f16_mx<NT, false>(at, it.sf, xr, g, t, undo, acc);
+                } else if (ONE) {
+                    item_f16_one(it, xr[0], g, t, one);
                 } else {
                     item_f16_nvfp4<NT>(it, xr, t, acc);
                 }
@@ -545,12 +585,14 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_kernel(const Params p) {
                 }
             };
             for (int slot = 0; item < end; slot = slot + 1 == kAhead ? 0 : slot + 1) {
-                copies_wait<kAhead - 1>();                  // a lane reads what it copied itself
+                copies_wait<kAhead - 1>();                  // a lane reads what it copied itself; MX: what the warp did
+                if (MX) __syncwarp();
                 Item it;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) it.codes[i] = load_shared(ring + slot * kItemBytes + i * 512);
                 it.sf = load_shared(ring + slot * kItemBytes + 4 * 512);
-                run(it);
+                run(it, items + slot * kItemBytes);
+                if (MX) __syncwarp();                       // before the slot is filled again
                 fetch(slot);
             }
             copies_wait<0>();
@@ -594,9 +636,9 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_kernel(const Params p) {
     }
 }
 
-template <int NT, bool MX>
+template <int NT, bool MX, bool ONE>
 cudaError_t launch(const Params& p, int clusters, int ranks, int smem, cudaStream_t stream) {
-    cudaError_t e = cudaFuncSetAttribute(gemv_kernel<NT, MX>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    cudaError_t e = cudaFuncSetAttribute(gemv_kernel<NT, MX, ONE>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)clusters, (unsigned)ranks);
@@ -610,7 +652,7 @@ cudaError_t launch(const Params& p, int clusters, int ranks, int smem, cudaStrea
     attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = ranks > 1 ? 1 : 0;
-    e = cudaLaunchKernelEx(&cfg, gemv_kernel<NT, MX>, p);
+    e = cudaLaunchKernelEx(&cfg, gemv_kernel<NT, MX, ONE>, p);
     if (e == cudaSuccess) count_launch(1);
     return e;
 }
@@ -624,8 +666,8 @@ int64_t resident_clusters(bool two, bool mx, int ranks, int num_sms) {
     std::atomic<int>& slot = known[dev][ranks == 8];
     int n = slot.load(std::memory_order_relaxed);
     if (n == 0) {
-        const void* kernel = two ? (mx ? (const void*)gemv_kernel<2, true> : (const void*)gemv_kernel<2, false>)
-                                 : (mx ? (const void*)gemv_kernel<1, true> : (const void*)gemv_kernel<1, false>);
+        const void* kernel = two ? (mx ? (const void*)gemv_kernel<2, true, false> : (const void*)gemv_kernel<2, false, false>)
+                                 : (mx ? (const void*)gemv_kernel<1, true, false> : (const void*)gemv_kernel<1, false, false>);
         if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit) != cudaSuccess) return 1;
         cudaLaunchConfig_t cfg{};
         cfg.gridDim = dim3((unsigned)num_sms, (unsigned)ranks);
@@ -687,8 +729,10 @@ cudaError_t launch_gemv(const GemvArgs& a, int num_sms, cudaStream_t stream) {
     if (p.unit_chunk > per) p.unit_chunk = per;
     const int smem = ring_bytes + x_bytes + (kWarps + p.unit_chunk) * unit_bytes;
     if (a.M <= 8)
-        return a.mx ? launch<1, true>(p, clusters, ranks, smem, stream) : launch<1, false>(p, clusters, ranks, smem, stream);
-    return a.mx ? launch<2, true>(p, clusters, ranks, smem, stream) : launch<2, false>(p, clusters, ranks, smem, stream);
+        return a.mx       ? launch<1, true, false>(p, clusters, ranks, smem, stream)
+               : a.M == 1 ? launch<1, false, true>(p, clusters, ranks, smem, stream)
+                          : launch<1, false, false>(p, clusters, ranks, smem, stream);
+    return a.mx ? launch<2, true, false>(p, clusters, ranks, smem, stream) : launch<2, false, false>(p, clusters, ranks, smem, stream);
 }
 
 }  // namespace nvfp4

@@ -114,8 +114,9 @@ def test_gemv_strided_rows_outputs_and_repeats(cuda_ok):
     assert torch.equal(out, y.bfloat16())
     for _ in range(3):                                      # the same bits every time
         assert torch.equal(nv.gemv_w4a16(x, w, out_dtype=torch.float32), y)
-    # one row of several rows' storage: its stride is not looked at
-    assert torch.equal(nv.gemv_w4a16(x[2:3], w, out_dtype=torch.float32), y[2:3])
+    # one row of several rows' storage: its stride is not looked at (a single row is summed in an order of its own, so
+    # its bits are those of a single row, not of the four)
+    assert torch.equal(_check(x[2:3], w), nv.gemv_w4a16(x[2:3].clone(), w, out_dtype=torch.float32))
     assert nv.gemv_w4a16(x[:0], w).shape == (0, 520)
 
 
@@ -172,3 +173,36 @@ def test_gemv_on_another_stream_and_in_a_graph(cuda_ok):
     g.replay()
     torch.cuda.synchronize()
     assert torch.equal(y, want2)
+
+
+@pytest.mark.parametrize("fmt", ["nvfp4", "mx"])
+@pytest.mark.parametrize("M", [1, 2, 8, 13])
+@pytest.mark.parametrize("binades", [8, 30, 31, 32, 60])
+def test_gemv_values_over_many_binades(cuda_ok, fmt, M, binades):
+    """Rows of x whose values span a given number of binades (on either side of
+    what FP16 holds exactly) at different magnitudes, zeros among them; E8M0
+    scales over as many, up to where FP32 ends."""
+    N, K = 140, 1152
+    g = torch.Generator(device="cuda").manual_seed(binades + M)
+    e = torch.randint(0, binades + 1, (M, K), generator=g, device="cuda").double() - binades
+    e[:, 0], e[:, 1] = 0, -binades
+    m = 1 + torch.randint(0, 128, (M, K), generator=g, device="cuda").double() / 128
+    x = m * torch.exp2(e + 7 * torch.arange(M, device="cuda")[:, None].double() - 20)
+    x = torch.where(torch.rand(M, K, generator=g, device="cuda") < 0.5, x, -x)
+    x[:, 5::17] = 0.0
+    x = x.bfloat16()
+    w = _weights(N, K, fmt, seed=binades)
+    if fmt == "mx":
+        w.sf.copy_(torch.randint(127, 128 + binades, (w.sf.numel(),), generator=g, device="cuda").to(torch.uint8))
+    _check(x, w)
+
+
+def test_gemv_scales_at_the_ends_of_their_range(cuda_ok):
+    """E8M0 scales of 2^100 beside small ones, in some units only."""
+    N, K = 256, 640
+    w = _weights(N, K, "mx", seed=3)
+    sf = torch.randint(100, 130, (w.sf.numel(),), device="cuda", dtype=torch.uint8)
+    sf[::97] = 227
+    w.sf.copy_(sf)
+    for M in (1, 5, 16):
+        _check(synth.random_bf16((M, K), seed=M).cuda(), w)
