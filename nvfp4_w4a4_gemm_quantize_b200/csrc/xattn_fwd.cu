@@ -22,7 +22,8 @@
 // and owns TMEM, 4-7 and 8-11 softmax and output of A and B, a thread per row.
 // The output goes out by TMA from the item's own Q tile: written from the
 // registers, a row per thread, it took 6400 cycles an item (a 128-byte line per
-// lane and store), as long as two steps.
+// lane and store), as long as two steps.  It is read out once the next item's
+// first P is stored, so that the wait for the last product has gone by.
 // Bound by the exponentials and the tensor core about equally at d = 128 (a
 // pair of 128 x 128 tiles costs 2048 cycles of either), by the exponentials below.
 #include "xattn.cuh"
@@ -107,7 +108,7 @@ xattn_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
                  const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ CUtensorMap tmap_o, const FwdParams p) {
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t q_full[kQBufs], q_empty[kQBufs], kv_full[kMaxRing], kv_empty[kMaxRing];
-    __shared__ __align__(8) uint64_t s_full[2], p_full[2], o_full[2], o_free[2], drain;
+    __shared__ __align__(8) uint64_t s_full[2], p_full[2], o_full[2], drain;
     __shared__ uint32_t kv_info[kMaxRing], tmem_base_sh;
     __shared__ int abort_sh;
 
@@ -131,7 +132,6 @@ xattn_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
             mbar_init(&s_full[g], 1);
             mbar_init(&p_full[g], 4);               // the group's warps
             mbar_init(&o_full[g], 1);
-            mbar_init(&o_free[g], 4);
         }
         mbar_init(&drain, 1);
         fence_barrier_init();
@@ -209,7 +209,7 @@ xattn_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
             const uint32_t idesc_o = idesc_kmn(dsteps * 16);
             RingAt kat{0, 0}, vat{1, 0};            // K and V tiles alternate in the ring
             RingAt qat{0, 0};
-            uint32_t uses[2] = {0, 0}, outs[2] = {0, 0};   // tiles and items of each group so far
+            uint32_t uses[2] = {0, 0};              // tiles of each group so far
             int q_buf[2] = {0, 0};
             bool ok = true;
 
@@ -246,9 +246,8 @@ xattn_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
 #pragma unroll
                 for (int g = 0; g < 2; ++g) {
                     if (g == 1 && !(cur & kInfoTwo)) continue;
-                    ok = ok && warp_wait(&p_full[g], uses[g] & 1u, wc) && (g == 1 || warp_wait(&kv_full[vat.slot], vat.phase, wc)) &&
-                         // the item's first product overwrites O_g: the previous one's has been read out
-                         (!(cur & kInfoFirst) || outs[g] == 0 || warp_wait(&o_free[g], (outs[g] - 1) & 1u, wc));
+                    // (an item's first P comes after the previous item's O_g has been read out)
+                    ok = ok && warp_wait(&p_full[g], uses[g] & 1u, wc) && (g == 1 || warp_wait(&kv_full[vat.slot], vat.phase, wc));
                     if (!ok) break;
                     ++uses[g];
                     if (g == 0 && (cur & kInfoZero)) zero_rest(ring + vat.slot * tile_bytes, n, p.chunks, lane);
@@ -256,10 +255,7 @@ xattn_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
                     product_tmem<8>(tmem + kColO + g * 128, tmem + kColS + g * 128, vt, idesc_o, (n + 15) >> 4,
                                     (cur & kInfoFirst) == 0);
                     if (g == 1 || !(cur & kInfoTwo)) commit(&kv_empty[vat.slot]);
-                    if (cur & kInfoLast) {
-                        commit(&o_full[g]);
-                        ++outs[g];
-                    }
+                    if (cur & kInfoLast) commit(&o_full[g]);
                     if (g == 0) nxt = describe();
                     if (ok && nxt && (g == 0 || (nxt & kInfoTwo))) ok = issue_s(nxt, g);
                 }
@@ -291,13 +287,54 @@ xattn_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
             stored = -1;
             __syncwarp();
         };
+        // the finished item whose O_g is still in TMEM
+        bool pending = false;
+        int out_b = 0, out_head = 0, out_q0 = 0, out_slot = 0;
+        float inv = 0.0f;
+        auto read_out = [&]() {
+            if (!warp_wait(&o_full[g], outs & 1u, wc)) return false;
+            ++outs;
+            tc_fence_after();
+            uint8_t* tile = smem + out_slot * tile_bytes;        // its last product is done
+            for (int c4 = 0; c4 < ochunks; ++c4) {
+                uint32_t o[32];
+                tmem_ld_32x32b_x32(to + c4 * 32, o);
+                tmem_ld_wait();
+                uint8_t* dst = tile + (c4 >> 1) * kChunk + r * 128;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+                        w[u] = pack_bf16(__uint_as_float(o[8 * i + 2 * u]) * inv, __uint_as_float(o[8 * i + 2 * u + 1]) * inv);
+                    *reinterpret_cast<uint4*>(dst + ((((c4 & 1) * 4 + i) ^ (r & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                if (out_q0 + quarter * 32 < p.Lq)
+                    for (int c = 0; c < p.chunks; ++c)
+                        tma_store_4d(&tmap_o, tile + c * kChunk + quarter * 32 * 128, c * 64, out_head * p.ao.h,
+                                     out_q0 + quarter * 32, out_b * p.ao.b);
+                bulk_commit_group();
+            }
+            stored = out_slot;
+            pending = false;
+            return true;
+        };
         Item item, following = item_of(p, blockIdx.x);      // read ahead by one item
         for (int it = blockIdx.x; ok && it < p.items; it += gridDim.x) {
             item = following;
             if (it + (int)gridDim.x < p.items) following = item_of(p, it + gridDim.x);
             const int slot = (q_at + g) % kQBufs;
             if (item.steps > 0) q_at = (q_at + (item.two ? 2 : 1)) % kQBufs;
-            if (g == 1 && !item.two) continue;
+            if (g == 1 && !item.two) {
+                // nothing to do, but the loader may come to need the tile of the last item this group had
+                if (pending && !(ok = read_out())) break;
+                release();
+                continue;
+            }
             float m = -INFINITY, l = 0.0f;
             for (int j = 0; j < item.steps; ++j, ++uses) {
                 if (!warp_wait(&s_full[g], uses & 1u, wc)) {
@@ -365,11 +402,12 @@ xattn_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
                         tmem_st_x32(to + c4 * 32, o);
                     }
                 }
+                if (pending && !(ok = read_out())) break;
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&p_full[g]);
-                if (j == 0) release();
+                if (j == 1 || item.steps == 1) release();
             }
             if (!ok) break;
             int head, q0;
@@ -384,41 +422,14 @@ xattn_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
                     for (int i = 0; i < p.d; i += 8) *reinterpret_cast<uint4*>(orow + i) = make_uint4(0, 0, 0, 0);
                 continue;
             }
-            if (!warp_wait(&o_full[g], outs & 1u, wc)) break;
-            ++outs;
-            tc_fence_after();
-            const float inv = __frcp_rn(l);
-            uint8_t* tile = smem + slot * tile_bytes;            // its last product is done
-            for (int c4 = 0; c4 < ochunks; ++c4) {
-                uint32_t o[32];
-                tmem_ld_32x32b_x32(to + c4 * 32, o);
-                tmem_ld_wait();
-                if (c4 == ochunks - 1) {
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&o_free[g]);
-                }
-                uint8_t* dst = tile + (c4 >> 1) * kChunk + r * 128;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    uint32_t w[4];
-#pragma unroll
-                    for (int u = 0; u < 4; ++u)
-                        w[u] = pack_bf16(__uint_as_float(o[8 * i + 2 * u]) * inv, __uint_as_float(o[8 * i + 2 * u + 1]) * inv);
-                    *reinterpret_cast<uint4*>(dst + ((((c4 & 1) * 4 + i) ^ (r & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
-                }
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-                if (q0 + quarter * 32 < p.Lq)
-                    for (int c = 0; c < p.chunks; ++c)
-                        tma_store_4d(&tmap_o, tile + c * kChunk + quarter * 32 * 128, c * 64, head * p.ao.h, q0 + quarter * 32,
-                                     item.b * p.ao.b);
-                bulk_commit_group();
-            }
-            stored = slot;
+            inv = __frcp_rn(l);
+            out_b = item.b;
+            out_head = head;
+            out_q0 = q0;
+            out_slot = slot;
+            pending = true;
         }
+        if (ok && pending) read_out();
         release();
         if (lane == 0) bulk_wait_group_read<0>();
     }
