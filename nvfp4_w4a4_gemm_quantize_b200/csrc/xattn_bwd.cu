@@ -3,8 +3,8 @@
 //
 //   P = 2^(c S - lse log2(e)), D_i = sum_c dO_ic O_ic, dS = P (dO V^T - D)
 //   dQ = scale dS K,  dK = scale dS^T Q,  dV = P^T dO
-// Three kernels: D (one pass over dO and O), dQ by query tiles, dK and dV by
-// key tiles.  S and dO V^T are computed in both of the latter, seven tile
+// Three kernels: D (one pass over dO and O, where the states are more than
+// one key tile), dQ by query tiles, dK and dV by key tiles.  S and dO V^T are computed in both of the latter, seven tile
 // products in place of five: the sums of either stay in tensor memory, so
 // nothing is added in global memory and the order of every sum is fixed.
 //
@@ -112,7 +112,7 @@ struct DqParams {
     MapAxes aq, ag, ak, av, ad;
     nvfp4_heads dq;
     const float* lse;
-    const float* delta;
+    float* delta;                             // D (ONE: out)
     const int32_t* kv_lens;
     float c, scale;                           // scale * log2(e), scale
     int H, Hkv, Lq, Lk, d;
@@ -161,25 +161,55 @@ struct DqWalk {
     }
 };
 
+// D of a row whose keys are all in this tile, sum P dP, which unlike sum dO O has no rounding of O in it (with few keys
+// dP is close to D, and that rounding the larger part of dS's error): each of the four warps of a row adds its n
+// columns, p the P of them, the sums meet in d_part.  Out of line, so that its registers are not the main loop's.
+// (d_part is written again after the next dP, which comes after every warp has used this one's D.)
+__device__ __noinline__ bool row_d(const float* p, uint32_t dp_at, int n, int g, int r, uint64_t* bar, uint32_t parity,
+                                   float (*d_part)[kRows], const WaitCtx& wc, float* d) {
+    float sum[2] = {0.0f, 0.0f};
+    if (n > 0) {
+        uint32_t dp[32];
+        tmem_ld_32x32b_x32(dp_at, dp);
+        tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            if (i < n) sum[i & 1] = fmaf(p[i], __uint_as_float(dp[i]), sum[i & 1]);
+    }
+    d_part[g][r] = sum[0] + sum[1];
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+    if (!warp_wait(bar, parity, wc)) return false;
+    *d = ((d_part[0][r] + d_part[1][r]) + d_part[2][r]) + d_part[3][r];
+    return true;
+}
+
 constexpr int kMaxQ = 4, kMaxK = 4, kMaxV = 4;
 constexpr uint32_t kDqS = 0, kDqP = 256, kDqO = 384;      // S: [128 (s & 1), + 128); dP; dQ
 
+// ONE: every sample has one key tile (Lk <= 128), and D is formed here; otherwise it comes from delta_kernel.
+template <bool ONE>
 __global__ void __launch_bounds__(kBwdThreads, 1)
 xattn_dq_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_g,
                 const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
                 const __grid_constant__ CUtensorMap tmap_dq, const DqParams p) {
-    extern __shared__ uint8_t smem_raw[];
+    extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ __align__(8) uint64_t q_full[kMaxQ], q_empty[kMaxQ], k_full[kMaxK], k_empty[kMaxK], v_full[kMaxV], v_empty[kMaxV];
     __shared__ __align__(8) uint64_t s_full[2], dp_full, ds_ready, dq_full, drain;
+    __shared__ __align__(8) uint64_t d_bar[4];
+    __shared__ float d_part[4][kRows];                      // [column group][row]
     __shared__ uint32_t k_info[kMaxK], tmem_base_sh;
     __shared__ int abort_sh;
 
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int tile_bytes = p.chunks * kChunk;
     uint8_t* k_tiles = smem + p.qbufs * tile_bytes;
     uint8_t* v_tiles = k_tiles + p.kbufs * tile_bytes;
     WaitCtx wc{&abort_sh, p.dev_status};
+    if ((smem_u32(smem) & 1023u) != 0u) {           // the swizzled layouts need it; the declaration asks for it
+        if (p.dev_status) *p.dev_status = (int)NVFP4_ERR_MISALIGNED;
+        return;
+    }
 
     if (threadIdx.x == 0) {
         abort_sh = 0;
@@ -200,6 +230,7 @@ xattn_dq_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
         mbar_init(&dp_full, 1);
         mbar_init(&ds_ready, kBwdWarps);
         mbar_init(&dq_full, 1);
+        for (int i = 0; i < 4; ++i) mbar_init(&d_bar[i], 4);
         mbar_init(&drain, 1);
         fence_barrier_init();
         tma_prefetch_desc(&tmap_q);
@@ -337,7 +368,7 @@ xattn_dq_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
         const int g = (warp - 4) >> 2, quarter = warp & 3, r = quarter * 32 + lane;
         const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
         const uint32_t tbase = tmem + lane_base + g * kBwdCols;
-        uint32_t step = 0, outs = 0;
+        uint32_t step = 0, outs = 0, singles = 0;
         bool ok = true;
 
         auto row_at = [&](const DqItem& i) {
@@ -391,7 +422,7 @@ xattn_dq_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
             const int64_t at = ((int64_t)i.b * p.H + i.h) * p.Lq + i.q0 + r;
             const bool have = i.q0 + r < p.Lq;
             l = have ? __ldg(p.lse + at) : INFINITY;
-            delta = have ? __ldg(p.delta + at) : 0.0f;
+            delta = have && !ONE ? __ldg(p.delta + at) : 0.0f;
         };
         DqItem prev, item, following;
         float lse = 0.0f, dl = 0.0f, next_lse = 0.0f, next_dl = 0.0f;
@@ -429,6 +460,14 @@ xattn_dq_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
                 }
                 if (!(ok = warp_wait(&dp_full, step & 1u, wc))) break;
                 tc_fence_after();
+                if (ONE) {
+                    float copy[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) copy[i] = __uint_as_float(v[i]);
+                    if (!(ok = row_d(copy, tp, n, g, r, &d_bar[quarter], singles & 1u, d_part, wc, &dl))) break;
+                    ++singles;
+                    if (g == 0 && item.q0 + r < p.Lq) p.delta[((int64_t)item.b * p.H + item.h) * p.Lq + item.q0 + r] = dl;
+                }
                 if (n > 0) {
                     uint32_t dp[32], w[16];
                     tmem_ld_32x32b_x32(tp, dp);
@@ -883,18 +922,24 @@ cudaError_t launch_cross_attention_backward(const CrossAttnArgs& a, int num_sms,
     cudaError_t e;
     int launches = 0;
     if (a.Lq > 0) {
-        const int64_t rows = (int64_t)a.B * a.Lq * a.H;
-        const int64_t per = kDeltaThreads / 16 * kDeltaRows;
-        delta_kernel<<<(unsigned)((rows + per - 1) / per), kDeltaThreads, 0, stream>>>(a.grad_out, a.out, delta, (int)rows, a.Lq, a.H, a.d);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        const bool one = ktiles <= 1;
+        if (!one) {
+            const int64_t rows = (int64_t)a.B * a.Lq * a.H;
+            const int64_t per = kDeltaThreads / 16 * kDeltaRows;
+            delta_kernel<<<(unsigned)((rows + per - 1) / per), kDeltaThreads, 0, stream>>>(a.grad_out, a.out, delta, (int)rows,
+                                                                                           a.Lq, a.H, a.d);
+            if ((e = cudaGetLastError()) != cudaSuccess) return e;
+            ++launches;
+        }
         DqParams p{aq, ag, ak, av, ad, a.dq, a.lse, delta, a.kv_lens, a.scale * kLog2e, a.scale, a.H, a.Hkv, a.Lq, a.Lk, a.d,
                    a.H / a.Hkv, qtiles, a.B * a.H * qtiles, chunks, chunks == 1 ? 4 : 3, chunks == 1 ? 4 : 3, chunks == 1 ? 4 : 1,
                    a.dev_status};
-        const int smem = (p.qbufs + p.kbufs + p.vbufs) * tile_bytes + 1024;
-        if ((e = prepare_kernel(reinterpret_cast<const void*>(xattn_dq_kernel), smem)) != cudaSuccess) return e;
-        xattn_dq_kernel<<<p.items < num_sms ? p.items : num_sms, kBwdThreads, smem, stream>>>(mq, mg, mk, mv, md, p);
+        const int smem = (p.qbufs + p.kbufs + p.vbufs) * tile_bytes;
+        const auto kernel = one ? xattn_dq_kernel<true> : xattn_dq_kernel<false>;
+        if ((e = prepare_kernel(reinterpret_cast<const void*>(kernel), smem)) != cudaSuccess) return e;
+        kernel<<<p.items < num_sms ? p.items : num_sms, kBwdThreads, smem, stream>>>(mq, mg, mk, mv, md, p);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
-        launches += 2;
+        ++launches;
     }
     if (plan.units > 0 && plan.splits > 0) {
         DkvParams p{aq, ag, ak, av, a.dk, a.dv, a.lse, delta, a.kv_lens, partial, a.scale * kLog2e, a.scale, a.H, a.Hkv, a.Lq, a.Lk,
