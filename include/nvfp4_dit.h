@@ -22,8 +22,9 @@ extern "C" {
  * scales: the conditioning path of a block (the adaLN modulation has one row
  * per sample), where nvfp4_gemm_w4a16 would compute a whole 256-row tile.
  *   y[m,n] = g * sum_k x[m,k] * e2m1(w[n,k]) * s[n, k / block]  (+ bias[n])
- * The weight e2m1 * s is formed exactly in bf16, products are added in FP32,
- * g and the bias are applied in FP32, and y is rounded once.
+ * Weights and products are exact (in FP16 with a row's values times a power of
+ * two where they span few enough binades, in bf16 otherwise), products are added
+ * in FP32, g and the bias are applied in FP32, and y is rounded once.
  * x_bf16    [M, K] bf16, row stride ld_x (ld_x >= K, ld_x % 8 == 0), 16-byte
  *           aligned; 1 <= M <= NVFP4_GEMV_MAX_ROWS (M == 0 is a no-op).
  * w_format  NVFP4_WEIGHTS_NVFP4: w_codes, w_sf, w_scale as nvfp4_quantize
@@ -32,8 +33,9 @@ extern "C" {
  *           (block 32, s = 2^(byte - 127), g = 1, w_scale ignored), K % 128 == 0.
  * bias      nullable device FP32 [N].
  * y         [M, N] contiguous in y_dtype (any N >= 1).
- * The K range of an output tile is split over the CTAs of a cluster, whose
- * sums are added in a fixed order: the same call gives the same bits.
+ * The K range is split over the warps of a CTA and the CTAs of a cluster, whose
+ * sums are added in a fixed order: the same call gives the same bits.  (How it is
+ * split depends on M, N and K: a row's bits may differ between calls of other M.)
  * One kernel on `stream`, no workspace.
  */
 enum { NVFP4_WEIGHTS_NVFP4 = 0, NVFP4_WEIGHTS_MX = 1 };
@@ -113,7 +115,8 @@ nvfp4_status nvfp4_cross_attention(const nvfp4_heads *q, const nvfp4_heads *k, c
  *   P = exp(scale q k^T - lse), D_i = sum_c grad_out[i,c] out[i,c],
  *   dS = P * (grad_out v^T - D) * scale:
  *   dv = P^T grad_out,  dq = dS k,  dk = dS^T q  (dk, dv summed over the query
- * heads that share a key / value head).  out and lse are the forward call's.
+ * heads that share a key / value head).  out and lse are the forward call's
+ * (where Lk <= 128, D is formed as sum_j P_ij dP_ij, and out is not read).
  * P and dS are rounded to bf16 for the products; sums are FP32.  Keys at or past
  * a sample's length get dk = dv = 0, queries of a sample of length 0 dq = 0.
  * Partial sums are joined in a fixed order: the same call gives the same bits.
