@@ -638,7 +638,8 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_kernel(const Params p) {
 
 template <int NT, bool MX, bool ONE>
 cudaError_t launch(const Params& p, int clusters, int ranks, int smem, cudaStream_t stream) {
-    cudaError_t e = cudaFuncSetAttribute(gemv_kernel<NT, MX, ONE>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    // always the same limit: it belongs to the kernel, and another thread may be about to launch with more
+    cudaError_t e = cudaFuncSetAttribute(gemv_kernel<NT, MX, ONE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)clusters, (unsigned)ranks);

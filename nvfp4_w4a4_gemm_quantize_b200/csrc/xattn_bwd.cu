@@ -894,8 +894,10 @@ BwdPlan plan_backward(int64_t B, int64_t H, int64_t Hkv, int64_t Lq, int64_t Lk,
     return p;
 }
 
-cudaError_t prepare_kernel(const void* kernel, int smem) {
-    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+// Dynamic shared memory a launch may ask for.  Always the same limit: it belongs to the kernel, and another thread may be
+// about to launch with more.
+cudaError_t prepare_kernel(const void* kernel, int most) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
 }
 
 }  // namespace xattn
@@ -936,7 +938,7 @@ cudaError_t launch_cross_attention_backward(const CrossAttnArgs& a, int num_sms,
                    a.dev_status};
         const int smem = (p.qbufs + p.kbufs + p.vbufs) * tile_bytes;
         const auto kernel = one ? xattn_dq_kernel<true> : xattn_dq_kernel<false>;
-        if ((e = prepare_kernel(reinterpret_cast<const void*>(kernel), smem)) != cudaSuccess) return e;
+        if ((e = prepare_kernel(reinterpret_cast<const void*>(kernel), 14 * kChunk)) != cudaSuccess) return e;
         kernel<<<p.items < num_sms ? p.items : num_sms, kBwdThreads, smem, stream>>>(mq, mg, mk, mv, md, p);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
         ++launches;
@@ -945,7 +947,7 @@ cudaError_t launch_cross_attention_backward(const CrossAttnArgs& a, int num_sms,
         DkvParams p{aq, ag, ak, av, a.dk, a.dv, a.lse, delta, a.kv_lens, partial, a.scale * kLog2e, a.scale, a.H, a.Hkv, a.Lq, a.Lk,
                     a.d, a.H / a.Hkv, qtiles, ktiles, (int)plan.steps, plan.splits, chunks, chunks == 1 ? 8 : 4, a.dev_status};
         const int smem = (2 + p.qbufs) * tile_bytes + 1024;
-        if ((e = prepare_kernel(reinterpret_cast<const void*>(xattn_dkv_kernel), smem)) != cudaSuccess) return e;
+        if ((e = prepare_kernel(reinterpret_cast<const void*>(xattn_dkv_kernel), 12 * kChunk + 1024)) != cudaSuccess) return e;
         xattn_dkv_kernel<<<(unsigned)(plan.units * plan.splits), kBwdThreads, smem, stream>>>(mq, mg, mk, mv, p);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
         ++launches;

@@ -475,7 +475,8 @@ cudaError_t launch_forward_tiles(const CrossAttnArgs& a, int num_sms, cudaStream
     if (p.ring > kMaxRing) p.ring = kMaxRing;
     p.dev_status = a.dev_status;
     const int smem = (kQBufs + p.ring) * tile_bytes + 1024;
-    cudaError_t e = cudaFuncSetAttribute(xattn_fwd_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    // always the same limit: it belongs to the kernel, and another thread may be about to launch with more
+    cudaError_t e = cudaFuncSetAttribute(xattn_fwd_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit - 2048);
     if (e != cudaSuccess) return e;
     xattn_fwd_kernel<<<p.items < num_sms ? p.items : num_sms, kThreads, smem, stream>>>(mq, mk, mv, mo, p);
     e = cudaGetLastError();

@@ -345,6 +345,41 @@ def test_calls_from_new_threads(cuda_ok):
     assert torch.equal(buf, out) and len(got) == 3 and all(torch.equal(a, b) for a, b in zip(got, want))
 
 
+def test_threads_with_other_head_widths(cuda_ok):
+    """Two threads on two streams, calls of different sizes of every kernel at
+    the same time: each gets its own answers, none is refused."""
+    jobs = [(_inputs(1, 130, 40, 2, 2, d, seed=d), _inputs(1, 3, 200, 2, 2, d, seed=d + 1)) for d in (64, 128)]
+    w = [nv.quantize(torch.randn(256, k, device="cuda").bfloat16()) for k in (128, 4096)]
+    x = [torch.randn(m, k, device="cuda").bfloat16() for m, k in ((1, 128), (16, 4096))]
+
+    def run(i):
+        res = []
+        for q, k, v, do in jobs[i]:
+            out, lse = nv.cross_attention(q, k, v, return_lse=True)
+            res += [out, *nv.cross_attention_backward(do, q, k, v, out, lse)]
+        return [*res, nv.gemv_w4a16(x[i], w[i])]
+
+    want, got, errors = [run(0), run(1)], [None, None], []
+    torch.cuda.synchronize()
+
+    def work(i):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(60):
+                    got[i] = run(i)
+        except Exception as e:                       # noqa: BLE001 - reported by the test
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not errors
+    assert all(torch.equal(a, b) for i in range(2) for a, b in zip(got[i], want[i]))
+
+
 @pytest.mark.parametrize("Lq", [1, 300])
 def test_two_streams_and_a_graph(cuda_ok, Lq):
     """Two calls at once on two streams; the training step captured and replayed

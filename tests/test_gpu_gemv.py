@@ -197,6 +197,13 @@ def test_gemv_values_over_many_binades(cuda_ok, fmt, M, binades):
     _check(x, w)
 
 
+@pytest.mark.parametrize("fmt,M,N,K", [("nvfp4", 16, 230016, 128), ("nvfp4", 8, 70, 20480), ("mx", 16, 64, 40960),
+                                       ("mx", 1, 40, 65536), ("nvfp4", 1, 40, 65536), ("nvfp4", 11, 33, 30016)])
+def test_gemv_more_than_shared_memory_holds(cuda_ok, fmt, M, N, K):
+    """Output widths whose sums, and rows of x whose parts, a block takes in several passes."""
+    _check(synth.random_bf16((M, K), seed=N).cuda(), _weights(N, K, fmt, seed=K))
+
+
 def test_gemv_scales_at_the_ends_of_their_range(cuda_ok):
     """E8M0 scales of 2^100 beside small ones, in some units only."""
     N, K = 256, 640
