@@ -8,7 +8,7 @@
 // Every warp is a stream of its own over a range of the keys: it loads slices of
 // 32 keys of K and V by TMA into a ring of its own and refills a slot when it has
 // used it, so nothing in the loop waits for another warp.  The keys of a (sample,
-// key / value head) are split over the four warps of a block and the blocks of a
+// key / value head) are split over the warps of a block and the blocks of a
 // cluster; their (maximum, sum, O) are joined in a fixed order, warps over shared,
 // blocks over distributed shared memory, without a workspace.
 #include "xattn.cuh"
@@ -16,8 +16,9 @@
 namespace nvfp4 {
 namespace xattn {
 
-constexpr int kFewWarps = 4;
-constexpr int kFewThreads = 32 * kFewWarps;
+// Warps of a block: their rings fill most of an SM's shared memory.
+template <int DS>
+constexpr int kWarpsOf = DS == 4 ? 8 : 4;
 constexpr int kSlice = 32;                    // keys of a slice
 constexpr int kSliceChunk = kSlice * 128;     // bytes of 64 of its columns
 constexpr int kFewStages = 3;
@@ -51,8 +52,9 @@ __device__ __forceinline__ void mma_m16n8k16(float (&c)[4], const uint32_t (&a)[
 
 // DS: steps of 16 columns kept in registers, at least ceil(d / 16).
 template <int DS>
-__global__ void __launch_bounds__(kFewThreads)
+__global__ void __launch_bounds__(32 * kWarpsOf<DS>)
 xattn_few_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v, const FewParams p) {
+    constexpr int kFewWarps = kWarpsOf<DS>, kFewThreads = 32 * kFewWarps;
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t full[kFewWarps][kFewStages];
     __shared__ float ms[kFewWarps][kFewRows], ls[kFewWarps][kFewRows];     // the warps' maxima (scaled, base 2) and sums
@@ -298,6 +300,7 @@ xattn_few_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
 
 template <int DS>
 cudaError_t launch_few_kernel(const CUtensorMap& mk, const CUtensorMap& mv, const FewParams& p, int pairs, int ranks, cudaStream_t stream) {
+    constexpr int kFewWarps = kWarpsOf<DS>, kFewThreads = 32 * kFewWarps;
     int smem = kFewWarps * kFewStages * 2 * p.chunks * kSliceChunk;
     const int join = kFewWarps * kFewRows * (DS * 16 + 8) * 4;
     if (smem < join) smem = join;
@@ -341,13 +344,14 @@ cudaError_t launch_forward_few(const CrossAttnArgs& a, int num_sms, cudaStream_t
     p.chunks = (a.d + 63) / 64;
     p.dev_status = a.dev_status;
     // Blocks along the keys: the number that ends first, counted in slices of a warp; a block's start and join cost
-    // about four, and two blocks fit an SM at d <= 64, one above.
+    // about four.  One block fits an SM.
     const int pairs = a.B * a.Hkv;
-    const int64_t slots = (int64_t)num_sms * (p.chunks == 1 ? 2 : 1), slices = (a.Lk + kSlice - 1) / kSlice;
+    const int warps = p.chunks == 1 ? kWarpsOf<4> : kWarpsOf<8>;
+    const int64_t slots = num_sms, slices = (a.Lk + kSlice - 1) / kSlice;
     int ranks = 1;
     int64_t best = 0;
     for (int r = 1; r <= kFewMaxCluster; r *= 2) {
-        const int64_t cost = ((int64_t)pairs * r + slots - 1) / slots * ((slices + r * kFewWarps - 1) / (r * kFewWarps) + 4);
+        const int64_t cost = ((int64_t)pairs * r + slots - 1) / slots * ((slices + r * warps - 1) / (r * warps) + 4);
         if (best == 0 || cost < best) {
             best = cost;
             ranks = r;
