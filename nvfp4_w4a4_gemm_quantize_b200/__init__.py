@@ -227,6 +227,11 @@ def _heads(t) -> bytes:
     return _PACK_HEADS(t.data_ptr(), sb, sl, sh)
 
 
+def _new_heads(t, L, H, d) -> bytes:
+    """The same of a contiguous tensor that the call allocated."""
+    return _PACK_HEADS(t.data_ptr(), L * H * d, H * d, d)
+
+
 @functools.lru_cache(maxsize=64)
 def _ints(values: tuple) -> bytes:
     return struct.pack(f"{len(values)}i", *values)
@@ -579,15 +584,15 @@ def gemv_w4a16(x: torch.Tensor, w: NVFP4Tensor | MXTensor, bias: torch.Tensor | 
         raise ValueError("x must be contiguous along k")
     if bias is not None and (bias.dtype is not torch.float32 or bias.shape != (N,) or not bias.is_contiguous()):
         raise ValueError("bias must be a contiguous FP32 [N]")
+    y_dtype = _DT.get(out_dtype if out is None else out.dtype)
+    if y_dtype is None:
+        raise ValueError("out must be a contiguous bf16 or FP32 [M, N]")
+    _on_device(x, codes, sf, scale, bias, out)
     if out is None:
         y = torch.empty(M, N, dtype=out_dtype, device=x.device)
     else:
         y = out
         _require(y.shape == (M, N) and y.is_contiguous(), "out must be a contiguous bf16 or FP32 [M, N]")
-    y_dtype = _DT.get(y.dtype)
-    if y_dtype is None:
-        raise ValueError("out must be a contiguous bf16 or FP32 [M, N]")
-    _on_device(x, codes, sf, scale, bias, y)
     check(lib().nvfp4_gemv_w4a16(x.data_ptr(), ld if ld > K else K, codes.data_ptr(), sf.data_ptr(),
                                  None if mx else scale.data_ptr(), NVFP4_WEIGHTS_MX if mx else NVFP4_WEIGHTS_NVFP4,
                                  None if bias is None else bias.data_ptr(), M, N, K, y.data_ptr(), y_dtype,
@@ -618,28 +623,34 @@ def rotary(x: torch.Tensor, positions: torch.Tensor, axes, theta: float = 10000.
     (``interleaved``) or halves of the turned part; ``inverse`` turns back.
     ``out``: any [B, L, H, d] view (for instance of a [B, H, L, d] buffer, whose
     rows quantize() takes), or x itself."""
-    dtype = _DT.get(x.dtype)
-    if dtype is None or x.dim() != 4 or x.stride(3) != 1:
+    dt, xs, st = x.dtype, x.shape, x.stride()
+    dtype = _DT.get(dt)
+    if dtype is None or len(xs) != 4 or st[3] != 1:
         raise ValueError("x must be bf16 or FP32 [B, L, H, d], d contiguous")
-    B, L, H, d = xs = x.shape
+    B, L, H, d = xs
     axes = tuple(axes)
-    ps, pt = positions.shape, positions.stride()
-    per_sample = len(ps) == 3 and ps[0] > 1
-    if not (positions.dtype in (torch.int32, torch.float32) and len(ps) in (2, 3) and ps[-2] == L and ps[-1] == len(axes)
-            and (len(ps) == 2 or ps[0] in (1, B))):
+    ps, pt, pd = positions.shape, positions.stride(), positions.dtype
+    n = len(ps)
+    per_sample = n == 3 and ps[0] > 1
+    if ((pd is not torch.int32 and pd is not torch.float32) or (n != 2 and n != 3) or ps[-2] != L or ps[-1] != len(axes)
+            or (per_sample and ps[0] != B) or (n == 3 and ps[0] == 0 != B)):
         raise ValueError("positions must be int32 or FP32 [L, n_axes] or [B, L, n_axes]")
     if pt[-1] != 1 and len(axes) != 1:
         raise ValueError("positions must be contiguous along the axes")
     if out is None:
-        y = torch.empty(B, L, H, d, dtype=x.dtype, device=x.device)
+        _on_device(x, positions)
+        y = torch.empty(B, L, H, d, dtype=dt, device=x.device)
+        to = _new_heads(y, L, H, d)
     else:
         y = out
-        _require(y.dtype == x.dtype and y.shape == xs and y.stride(3) == 1, "out must match x, d contiguous")
-    _on_device(x, positions, y)
+        _require(y.dtype == dt and y.shape == xs and y.stride(3) == 1, "out must match x, d contiguous")
+        _on_device(x, positions, y)
+        to = _heads(y)
     flags = (NVFP4_ROTARY_INTERLEAVED if interleaved else 0) | (NVFP4_ROTARY_INVERSE if inverse else 0)
-    check(lib().nvfp4_rotary(_heads(x), positions.data_ptr(), NVFP4_POSITION_I32 if positions.dtype is torch.int32 else
-                             NVFP4_POSITION_F32, pt[0] if per_sample else 0, pt[-2], _ints(axes), len(axes), float(theta), B, L,
-                             H, d, dtype, flags, _heads(y), _stream(stream)), "nvfp4_rotary")
+    check(lib().nvfp4_rotary(_PACK_HEADS(x.data_ptr(), st[0], st[1], st[2]), positions.data_ptr(),
+                             NVFP4_POSITION_I32 if pd is torch.int32 else NVFP4_POSITION_F32, pt[0] if per_sample else 0,
+                             pt[-2], _ints(axes), len(axes), float(theta), B, L, H, d, dtype, flags, to, _stream(stream)),
+          "nvfp4_rotary")
     if out is None and stream is not None:
         _used_on(stream, y)
     return y
@@ -686,14 +697,17 @@ def cross_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, kv_lens: 
     [B, H, Lq] log-sum-exp that cross_attention_backward() takes."""
     B, H, Hkv, Lq, Lk, d = _attention_sizes(q, k, v, kv_lens)
     if out is None:
+        _on_device(q, k, v, kv_lens, dev_status)
         o = torch.empty(B, Lq, H, d, dtype=torch.bfloat16, device=q.device)
+        to = _new_heads(o, Lq, H, d)
     else:
         o = out
         _require(o.dtype == torch.bfloat16 and o.shape == q.shape and o.stride(3) == 1, "out must be a bf16 tensor of q's shape")
+        _on_device(q, k, v, kv_lens, o, dev_status)
+        to = _heads(o)
     lse = torch.empty(B, H, Lq, dtype=torch.float32, device=q.device) if return_lse else None
-    _on_device(q, k, v, kv_lens, o, dev_status)
     check(lib().nvfp4_cross_attention(_heads(q), _heads(k), _heads(v), None if kv_lens is None else kv_lens.data_ptr(),
-                                      d ** -0.5 if scale is None else float(scale), B, H, Hkv, Lq, Lk, d, _heads(o),
+                                      d ** -0.5 if scale is None else float(scale), B, H, Hkv, Lq, Lk, d, to,
                                       None if lse is None else lse.data_ptr(), _ptr(dev_status), _stream(stream)),
           "nvfp4_cross_attention")
     if stream is not None:
@@ -727,7 +741,7 @@ def cross_attention_backward(grad_out: torch.Tensor, q: torch.Tensor, k: torch.T
     check(lib().nvfp4_cross_attention_backward(
         _heads(grad_out), _heads(q), _heads(k), _heads(v), _heads(out), lse.data_ptr(),
         None if kv_lens is None else kv_lens.data_ptr(), d ** -0.5 if scale is None else float(scale), B, H, Hkv, Lq, Lk, d,
-        _heads(dq), _heads(dk), _heads(dv), ws.data_ptr(), bytes_, _ptr(dev_status), _stream(stream)),
+        _new_heads(dq, Lq, H, d), _new_heads(dk, Lk, Hkv, d), _new_heads(dv, Lk, Hkv, d), ws.data_ptr(), bytes_, _ptr(dev_status), _stream(stream)),
         "nvfp4_cross_attention_backward")
     if stream is not None:
         _used_on(stream, dq, dk, dv, *((ws,) if workspace is None else ()))
