@@ -130,6 +130,15 @@ __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uin
 
 constexpr uint32_t kTwo119 = 0x7B007B00u, kTwo120 = 0x7B807B80u;   // bf16 pairs
 
+// The same in FP16, started from zero.
+__device__ __forceinline__ void mma_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                          uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                 "{%10, %10, %10, %10};"
+                 : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
+
 // Scales of a lane's 32 k of one feature.
 //   NVFP4: two blocks; e4m3 times 2^119 as bf16 pairs.  A byte moved to bf16's
 //     exponent and mantissa reads as the scale times 2^-120 (subnormals too).
@@ -210,7 +219,7 @@ __device__ __forceinline__ void item_f16_nvfp4(const Item& it, const uint8_t* co
 // One item of one row in FP16, NVFP4: the eight columns of B hold the row's eight blocks, each lane column's 32 k its
 // two (zeros elsewhere), so a product's sums come apart by block and the scales are applied to them in FP32.
 __device__ __forceinline__ void item_f16_one(const Item& it, const uint8_t* xrow, int g, int t, float (&acc)[4]) {
-    float sum[2][4] = {};
+    float sum[2][4];
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
         uint4 b = make_uint4(0, 0, 0, 0);
@@ -220,7 +229,8 @@ __device__ __forceinline__ void item_f16_one(const Item& it, const uint8_t* xrow
             uint32_t f[2][4];
             decode_f16(word_of(it.codes[2 * u], w), f[0]);
             decode_f16(word_of(it.codes[2 * u + 1], w), f[1]);
-            mma<true>(sum[u], f[0][0], f[1][0], f[0][1], f[1][1], b.x, b.y);
+            if (w == 0) mma_first(sum[u], f[0][0], f[1][0], f[0][1], f[1][1], b.x, b.y);
+            else mma<true>(sum[u], f[0][0], f[1][0], f[0][1], f[1][1], b.x, b.y);
             mma<true>(sum[u], f[0][2], f[1][2], f[0][3], f[1][3], b.z, b.w);
         }
     }
@@ -237,7 +247,7 @@ __device__ __forceinline__ void item_f16_one(const Item& it, const uint8_t* xrow
 }
 
 // One item in FP16, MX: a block's 32 k are one 16-byte piece of a feature, of which lane t takes word t, so that a
-// product's sums are of one block and its scale is applied to them in FP32, times 2^(byte - 128).  Pieces lie in the
+// product's sums are of one block and its scale is applied to them in FP32.  Pieces lie in the
 // order the copies gave them: (4 g + (block ^ (g / 2 & 3))) 16 bytes into the feature's 512.
 // SAFE: the rows' powers of two are undone first (see below).
 template <int NT, bool SAFE>
@@ -256,13 +266,18 @@ __device__ __forceinline__ void item_f16_mx(uint32_t item, const uint4& sf, cons
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 decode_f16(load_shared_word(at + (2 * u + i) * 512), f[i]);
-                const uint32_t e = (word_of(sf, 2 * u + i) >> (8 * c)) & 0xFFu;
-                s[i] = __uint_as_float(e > 1u ? (e - 1u) << 23 : 0x00200000u << e);
+                const uint32_t word = word_of(sf, 2 * u + i);
+                if (SAFE) {                         // 2^(byte - 128), so that 2^128 is not needed
+                    const uint32_t e = (word >> (8 * c)) & 0xFFu;
+                    s[i] = __uint_as_float(e > 1u ? (e - 1u) << 23 : 0x00200000u << e);
+                } else {                            // 2^(byte - 127)
+                    s[i] = __uint_as_float(max((c < 3 ? word << (23 - 8 * c) : word >> 1) & 0x7F800000u, 0x00400000u));
+                }
             }
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
-                float sum[4] = {};
-                mma<true>(sum, f[0][0], f[1][0], f[0][1], f[1][1], b[j].x, b[j].y);
+                float sum[4];
+                mma_first(sum, f[0][0], f[1][0], f[0][1], f[1][1], b[j].x, b[j].y);
                 mma<true>(sum, f[0][2], f[1][2], f[0][3], f[1][3], b[j].z, b[j].w);
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
@@ -522,8 +537,8 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_kernel(const Params p) {
                     for (int c = 0; c < 2; ++c) {
                         const int row = 8 * j + 2 * t + c;
                         if (row >= a.M) continue;
-                        // the bf16 path's NVFP4 weights are 2^-7 of theirs, the FP16 path's E8M0 scales half of theirs
-                        const float by = fits ? (MX ? (raised ? 2.0f : 2.0f * undo[j][c]) : undo[j][c]) : (MX ? 1.0f : 128.0f);
+                        // the bf16 path's NVFP4 weights are 2^-7 of theirs, E8M0 scales of raised units half of theirs
+                        const float by = fits ? (MX ? (raised ? 2.0f : undo[j][c]) : undo[j][c]) : (MX ? 1.0f : 128.0f);
 #pragma unroll
                         for (int u = 0; u < 2; ++u)
 #pragma unroll
@@ -552,7 +567,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_kernel(const Params p) {
 #pragma unroll
                             for (int j = 0; j < NT; ++j)
 #pragma unroll
-                                for (int e = 0; e < 4; ++e) acc[u][j][e] *= undo[j][e & 1];
+                                for (int e = 0; e < 4; ++e) acc[u][j][e] *= 0.5f * undo[j][e & 1];
                 }
                 if (!fits || raised) {
                     Item copy = it;
@@ -588,8 +603,11 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_kernel(const Params p) {
                 copies_wait<kAhead - 1>();                  // a lane reads what it copied itself; MX: what the warp did
                 if (MX) __syncwarp();
                 Item it;
+                auto load_codes = [&]() {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) it.codes[i] = load_shared(ring + slot * kItemBytes + i * 512);
+                    for (int i = 0; i < 4; ++i) it.codes[i] = load_shared(ring + slot * kItemBytes + i * 512);
+                };
+                if (!MX || !fits) load_codes();             // item_f16_mx reads them where they are
                 it.sf = load_shared(ring + slot * kItemBytes + 4 * 512);
                 run(it, items + slot * kItemBytes);
                 if (MX) __syncwarp();                       // before the slot is filled again
