@@ -259,6 +259,7 @@ def nvfp4_cross_attention(q, k, v, kv_lens, scale, B, H, Hkv, Lq, Lk, d, out, ls
           "nvfp4_cross_attention")
 
 
+@functools.lru_cache(maxsize=256)                      # of its sizes alone
 def nvfp4_cross_attention_backward_workspace_bytes(B: int, H: int, Hkv: int, Lq: int, Lk: int, d: int) -> int:
     return int(lib().nvfp4_cross_attention_backward_workspace_bytes(B, H, Hkv, Lq, Lk, d))
 
@@ -741,8 +742,8 @@ def cross_attention_backward(grad_out: torch.Tensor, q: torch.Tensor, k: torch.T
     check(lib().nvfp4_cross_attention_backward(
         _heads(grad_out), _heads(q), _heads(k), _heads(v), _heads(out), lse.data_ptr(),
         None if kv_lens is None else kv_lens.data_ptr(), d ** -0.5 if scale is None else float(scale), B, H, Hkv, Lq, Lk, d,
-        _new_heads(dq, Lq, H, d), _new_heads(dk, Lk, Hkv, d), _new_heads(dv, Lk, Hkv, d), ws.data_ptr(), bytes_, _ptr(dev_status), _stream(stream)),
-        "nvfp4_cross_attention_backward")
+        _new_heads(dq, Lq, H, d), _new_heads(dk, Lk, Hkv, d), _new_heads(dv, Lk, Hkv, d), ws.data_ptr(), bytes_,
+        _ptr(dev_status), _stream(stream)), "nvfp4_cross_attention_backward")
     if stream is not None:
         _used_on(stream, dq, dk, dv, *((ws,) if workspace is None else ()))
     return dq, dk, dv

