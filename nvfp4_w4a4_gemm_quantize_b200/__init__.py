@@ -675,17 +675,18 @@ class RotaryEmbedding(torch.autograd.Function):
         return rotary(_rows16(grad), positions, *ctx.how, inverse=True), None, None, None, None
 
 
-def _attention_sizes(q, k, v, kv_lens):
-    qs, ks, bf16 = q.shape, k.shape, torch.bfloat16
+def _attention_operands(q, k, v, kv_lens):
+    """(B, H, Hkv, Lq, Lk, d) and q, k, v as nvfp4_heads."""
+    qs, ks, qt, kt, vt, bf16 = q.shape, k.shape, q.stride(), k.stride(), v.stride(), torch.bfloat16
     if len(qs) != 4 or len(ks) != 4 or v.shape != ks or ks[0] != qs[0] or ks[3] != qs[3]:
         raise ValueError("q must be [B, Lq, H, d], k and v [B, Lk, Hkv, d]")
-    if (q.dtype is not bf16 or k.dtype is not bf16 or v.dtype is not bf16 or q.stride(3) != 1 or k.stride(3) != 1 or
-            v.stride(3) != 1):
+    if (q.dtype is not bf16 or k.dtype is not bf16 or v.dtype is not bf16 or qt[3] != 1 or kt[3] != 1 or vt[3] != 1):
         raise ValueError("q, k and v must be bf16, d contiguous")
     B, Lq, H, d = qs
     if kv_lens is not None and (kv_lens.dtype is not torch.int32 or kv_lens.shape != (B,) or not kv_lens.is_contiguous()):
         raise ValueError("kv_lens must be a contiguous int32 [B]")
-    return B, H, ks[2], Lq, ks[1], d
+    return ((B, H, ks[2], Lq, ks[1], d), _PACK_HEADS(q.data_ptr(), qt[0], qt[1], qt[2]),
+            _PACK_HEADS(k.data_ptr(), kt[0], kt[1], kt[2]), _PACK_HEADS(v.data_ptr(), vt[0], vt[1], vt[2]))
 
 
 def cross_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, kv_lens: torch.Tensor | None = None,
@@ -696,7 +697,7 @@ def cross_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, kv_lens: 
     kv_lens[b] keys of sample b (all of them without kv_lens).  scale defaults
     to 1 / sqrt(d).  Returns bf16 [B, Lq, H, d], and with ``return_lse`` the FP32
     [B, H, Lq] log-sum-exp that cross_attention_backward() takes."""
-    B, H, Hkv, Lq, Lk, d = _attention_sizes(q, k, v, kv_lens)
+    (B, H, Hkv, Lq, Lk, d), hq, hk, hv = _attention_operands(q, k, v, kv_lens)
     if out is None:
         _on_device(q, k, v, kv_lens, dev_status)
         o = torch.empty(B, Lq, H, d, dtype=torch.bfloat16, device=q.device)
@@ -707,7 +708,7 @@ def cross_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, kv_lens: 
         _on_device(q, k, v, kv_lens, o, dev_status)
         to = _heads(o)
     lse = torch.empty(B, H, Lq, dtype=torch.float32, device=q.device) if return_lse else None
-    check(lib().nvfp4_cross_attention(_heads(q), _heads(k), _heads(v), None if kv_lens is None else kv_lens.data_ptr(),
+    check(lib().nvfp4_cross_attention(hq, hk, hv, None if kv_lens is None else kv_lens.data_ptr(),
                                       d ** -0.5 if scale is None else float(scale), B, H, Hkv, Lq, Lk, d, to,
                                       None if lse is None else lse.data_ptr(), _ptr(dev_status), _stream(stream)),
           "nvfp4_cross_attention")
@@ -721,10 +722,12 @@ def cross_attention_backward(grad_out: torch.Tensor, q: torch.Tensor, k: torch.T
                              scale: float | None = None, workspace: torch.Tensor | None = None, dev_status=None,
                              stream=None):
     """(dq, dk, dv) of cross_attention() from its ``out`` and ``lse``."""
-    B, H, Hkv, Lq, Lk, d = sizes = _attention_sizes(q, k, v, kv_lens)
+    sizes, hq, hk, hv = _attention_operands(q, k, v, kv_lens)
+    B, H, Hkv, Lq, Lk, d = sizes
     shape, bf16, device = q.shape, torch.bfloat16, q.device
+    gt, ot = grad_out.stride(), out.stride()
     if (grad_out.dtype is not bf16 or out.dtype is not bf16 or grad_out.shape != shape or out.shape != shape or
-            grad_out.stride(3) != 1 or out.stride(3) != 1):
+            gt[3] != 1 or ot[3] != 1):
         raise ValueError("grad_out and out must be bf16 tensors of q's shape, d contiguous")
     if lse.dtype is not torch.float32 or lse.shape != (B, H, Lq) or not lse.is_contiguous():
         raise ValueError("lse must be a contiguous FP32 [B, H, Lq]")
@@ -740,7 +743,8 @@ def cross_attention_backward(grad_out: torch.Tensor, q: torch.Tensor, k: torch.T
     dv = torch.empty(B, Lk, Hkv, d, dtype=bf16, device=device)
     _on_device(grad_out, q, k, v, out, lse, kv_lens, ws, dev_status)
     check(lib().nvfp4_cross_attention_backward(
-        _heads(grad_out), _heads(q), _heads(k), _heads(v), _heads(out), lse.data_ptr(),
+        _PACK_HEADS(grad_out.data_ptr(), gt[0], gt[1], gt[2]), hq, hk, hv, _PACK_HEADS(out.data_ptr(), ot[0], ot[1], ot[2]),
+        lse.data_ptr(),
         None if kv_lens is None else kv_lens.data_ptr(), d ** -0.5 if scale is None else float(scale), B, H, Hkv, Lq, Lk, d,
         _new_heads(dq, Lq, H, d), _new_heads(dk, Lk, Hkv, d), _new_heads(dv, Lk, Hkv, d), ws.data_ptr(), bytes_,
         _ptr(dev_status), _stream(stream)), "nvfp4_cross_attention_backward")
