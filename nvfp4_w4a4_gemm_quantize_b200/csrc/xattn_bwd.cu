@@ -9,9 +9,12 @@
 // of either stay in tensor memory, so nothing is added in global memory and the
 // order of every sum is fixed.
 // B200, 2 x 8192 queries x (512, 389) states, 24 heads of 128: D 35 us (its bytes
-// 31), dQ 159, dK and dV 175, their join 20.  dK and dV's products keep the tensor
-// core 58 % busy (a large matrix product alone: 71 %); dQ's step of 2850 cycles
-// has 2160 of products at that rate.
+// 31), dQ 159, dK and dV 175, their join 20.  A step of dQ takes 2850 cycles, 1536
+// of them the tensor core's, one of dK and dV 3300, 2048 of them (58 % busy): the
+// one issuing warp shares its scheduler with busy warps, and its waits on barriers
+// that are complete take 170 to 290 cycles each.  (Two issuing warps, one a pair of
+// products, were slower, 217 us for dK and dV: their products alternate on the
+// tensor core.)
 //
 // dQ (dq_kernel): persistent, a work item is a 128-query tile of one head, its
 // steps are key tiles of 128.  TMEM: two S, one dP = dO V^T, dQ.  dS overwrites

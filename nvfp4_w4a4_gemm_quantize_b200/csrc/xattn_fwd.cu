@@ -25,9 +25,10 @@
 // lane and store), as long as two steps.  It is read out once the next item's
 // first P is stored, so that the wait for the last product has gone by.
 // Bound by a tile's chain, softmax -> P V -> next S -> softmax, 3800 cycles a pair
-// of tiles: the exponentials alone take 2048 of a pair, its products at d = 128
-// 2880 at the rate that the tensor core holds with every SM busy, and each of the
-// hand-overs between warps and tensor core 200 to 300.
+// of tiles: the exponentials take 2048 of a pair and its products at d = 128 as
+// much, but the two tiles' exponentials overlap in part, each hand-over between
+// warps and tensor core takes 200 to 300, and the issuing warp, next to busy ones,
+// needs about as long for a product as the tensor core.
 // B200, 32768 queries x 512 states, 24 heads of 128: 209 us (986 TFLOP/s).
 #include "xattn.cuh"
 
@@ -35,7 +36,8 @@ namespace nvfp4 {
 namespace xattn {
 
 constexpr int kThreads = 384;
-constexpr int kQBufs = 4;
+constexpr int kQBufs = 4;                     // two items' tiles: an output leaves from its own during the next item's steps
+static_assert(kQBufs >= 4, "an item would wait for the tiles of the one before it, and that one for this item");
 constexpr int kMaxRing = 12;
 // Of eight pairs of exponentials, on the FMA pipes.  32768 queries x 512 states, 24 heads of 128, with 0 to 3: 242, 235,
 // 247, 266 us (two softmax warps per scheduler: more is bound by their instructions).
