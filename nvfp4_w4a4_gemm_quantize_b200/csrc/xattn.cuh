@@ -249,9 +249,23 @@ __device__ __forceinline__ F2 ex2_pair(F2 x, int i) {
     return {ex2(x.x), ex2(x.y)};
 }
 
-// The whole warp waits; false once the block gives up.
+// The whole warp waits (as mbar_wait, with its limit); false once the block gives
+// up.  Every branch is on a vote, so that the code around it stays convergent.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const WaitCtx& w) {
-    return __all_sync(0xffffffffu, mbar_wait(bar, parity, w) ? 1 : 0) != 0;
+    const uint32_t at = smem_u32(bar);
+    if (__all_sync(0xffffffffu, mbar_try_wait(at, parity))) return true;
+    const uint64_t t0 = globaltimer_ns();
+    uint32_t n = 0;
+    while (true) {
+        if (__all_sync(0xffffffffu, mbar_try_wait(at, parity))) return true;
+        if ((++n & 255u) == 0u) {
+            if (__any_sync(0xffffffffu, *w.abort_flag)) return false;
+            if (__any_sync(0xffffffffu, globaltimer_ns() - t0 > kWaitLimitNs)) {
+                report_timeout(w);
+                return false;
+            }
+        }
+    }
 }
 
 }  // namespace xattn
