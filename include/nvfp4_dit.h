@@ -116,7 +116,7 @@ nvfp4_status nvfp4_cross_attention(const nvfp4_heads *q, const nvfp4_heads *k, c
  *   dS = P * (grad_out v^T - D) * scale:
  *   dv = P^T grad_out,  dq = dS k,  dk = dS^T q  (dk, dv summed over the query
  * heads that share a key / value head).  out and lse are the forward call's
- * (where Lk <= 128, D is formed as sum_j P_ij dP_ij, and out is not read).
+ * (for a sample of at most 128 keys D is formed as sum_j P_ij dP_ij, without out).
  * P and dS are rounded to bf16 for the products; sums are FP32.  Keys at or past
  * a sample's length get dk = dv = 0, queries of a sample of length 0 dq = 0.
  * Partial sums are joined in a fixed order: the same call gives the same bits.

@@ -4,7 +4,8 @@
 //   P = 2^(c S - lse log2(e)), D_i = sum_c dO_ic O_ic, dS = P (dO V^T - D)
 //   dQ = scale dS K,  dK = scale dS^T Q,  dV = P^T dO
 // Three kernels: D (one pass over dO and O, where the states are more than one
-// key tile), dQ by query tiles, dK and dV by key tiles.  S and dO V^T are
+// key tile), dQ by query tiles (apart for samples of more key tiles and of one,
+// which forms its D itself), dK and dV by key tiles.  S and dO V^T are
 // computed in both of the latter, seven tile products in place of five: the sums
 // of either stay in tensor memory, so nothing is added in global memory and the
 // order of every sum is fixed.
@@ -120,12 +121,13 @@ struct DqParams {
     MapAxes aq, ag, ak, av, ad;
     nvfp4_heads dq;
     const float* lse;
-    float* delta;                             // D (ONE: out)
+    float* delta;                             // D (out for samples of one key tile)
     const int32_t* kv_lens;
     float c, scale;                           // scale * log2(e), scale
     int H, Hkv, Lq, Lk, d;
     int group, qtiles, items;
     int chunks, qbufs, kbufs, vbufs;
+    bool zeros;                               // dQ of samples without keys is this launch's
     int* dev_status;
 };
 
@@ -144,27 +146,30 @@ __device__ __forceinline__ DqItem dq_item(const DqParams& p, int it) {
     return r;
 }
 
+// The next item at or after `it` (in this block's stride) that the kernel takes: ONE those of one step, the other of more.
+template <bool ONE>
 __device__ __forceinline__ int dq_next(const DqParams& p, int it, DqItem& item) {
     for (; it < p.items; it += gridDim.x) {
         item = dq_item(p, it);
-        if (item.steps > 0) break;
+        if (ONE ? item.steps == 1 : item.steps > 1) break;
     }
     return it;
 }
 
 // A walk over the steps of this block's items, in order.
+template <bool ONE>
 struct DqWalk {
     int it, j;
     DqItem item;
     __device__ void start(const DqParams& p) {
         j = 0;
-        it = dq_next(p, blockIdx.x, item);
+        it = dq_next<ONE>(p, blockIdx.x, item);
     }
     __device__ bool valid(const DqParams& p) const { return it < p.items; }
     __device__ void next(const DqParams& p) {
         if (++j == item.steps) {
             j = 0;
-            it = dq_next(p, it + gridDim.x, item);
+            it = dq_next<ONE>(p, it + gridDim.x, item);
         }
     }
 };
@@ -195,7 +200,7 @@ __device__ __noinline__ bool row_d(const float* p, uint32_t dp_at, int n, int g,
 constexpr int kMaxQ = 4, kMaxK = 4, kMaxV = 4;
 constexpr uint32_t kDqS = 0, kDqP = 256, kDqO = 384;      // S: [128 (s & 1), + 128); dP; dQ
 
-// ONE: every sample has one key tile (Lk <= 128), and D is formed here; otherwise it comes from delta_kernel.
+// ONE: the samples of one key tile, whose D is formed here; the others' comes from delta_kernel.
 template <bool ONE>
 __global__ void __launch_bounds__(kBwdThreads, 1)
 xattn_dq_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_g,
@@ -217,6 +222,16 @@ xattn_dq_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
     if ((smem_u32(smem) & 1023u) != 0u) {           // the swizzled layouts need it; the declaration asks for it
         if (p.dev_status) *p.dev_status = (int)NVFP4_ERR_MISALIGNED;
         return;
+    }
+
+    if (ONE && !p.zeros) {                          // beside a launch for longer samples: often there is nothing to do
+        int any = 0;
+        const int samples = p.items / (p.H * p.qtiles);
+        for (int b = threadIdx.x; b < samples; b += kBwdThreads) {
+            const int keys = keys_of(p.kv_lens, b, p.Lk);
+            any |= keys > 0 && keys <= kRows;
+        }
+        if (!__syncthreads_or(any)) return;
     }
 
     if (threadIdx.x == 0) {
@@ -261,7 +276,7 @@ xattn_dq_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
         if (warp == 0) {
             // -------------------------------------------------------- loads: Q, K, dO, V of an item, then K and V of its steps
             TileRing rq(p.qbufs), rk(p.kbufs), rv(p.vbufs);
-            DqWalk w;
+            DqWalk<ONE> w;
             bool ok = true;
             auto load = [&](TileRing& ring, uint64_t* full, uint64_t* empty, uint8_t* tiles, const CUtensorMap* map, int h, int l,
                             int b, uint32_t* info, uint32_t value) {
@@ -439,10 +454,11 @@ xattn_dq_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
         for (int it = blockIdx.x; ok && it < p.items; it += gridDim.x, item = following, lse = next_lse, dl = next_dl) {
             if (it + (int)gridDim.x < p.items) fetch(it + gridDim.x, following, next_lse, next_dl);
             if (item.steps == 0) {
-                if (item.q0 + r < p.Lq)
+                if (p.zeros && item.q0 + r < p.Lq)
                     for (int i = 0; i < cols; i += 8) *reinterpret_cast<uint4*>(row_at(item) + i) = make_uint4(0, 0, 0, 0);
                 continue;
             }
+            if (ONE != (item.steps == 1)) continue;
             const float lse2 = lse * kLog2e;
             for (int j = 0; j < item.steps; ++j, ++step) {
                 const int n = min(max(item.keys - j * kRows - g * kBwdCols, 0), kBwdCols);      // this warp's keys
@@ -932,8 +948,7 @@ cudaError_t launch_cross_attention_backward(const CrossAttnArgs& a, int num_sms,
     cudaError_t e;
     int launches = 0;
     if (a.Lq > 0) {
-        const bool one = ktiles <= 1;
-        if (!one) {
+        if (ktiles > 1) {
             const int64_t rows = (int64_t)a.B * a.Lq * a.H;
             const int64_t per = kDeltaThreads / 16 * kDeltaRows;
             delta_kernel<<<(unsigned)((rows + per - 1) / per), kDeltaThreads, 0, stream>>>(a.grad_out, a.out, delta, (int)rows,
@@ -943,13 +958,19 @@ cudaError_t launch_cross_attention_backward(const CrossAttnArgs& a, int num_sms,
         }
         DqParams p{aq, ag, ak, av, ad, a.dq, a.lse, delta, a.kv_lens, a.scale * kLog2e, a.scale, a.H, a.Hkv, a.Lq, a.Lk, a.d,
                    a.H / a.Hkv, qtiles, a.B * a.H * qtiles, chunks, chunks == 1 ? 4 : 3, chunks == 1 ? 4 : 3, chunks == 1 ? 4 : 1,
-                   a.dev_status};
+                   true, a.dev_status};
         const int smem = (p.qbufs + p.kbufs + p.vbufs) * tile_bytes;
-        const auto kernel = one ? xattn_dq_kernel<true> : xattn_dq_kernel<false>;
-        if ((e = prepare_kernel(reinterpret_cast<const void*>(kernel), 14 * kChunk)) != cudaSuccess) return e;
-        kernel<<<p.items < num_sms ? p.items : num_sms, kBwdThreads, smem, stream>>>(mq, mg, mk, mv, md, p);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
-        ++launches;
+        // samples of several key tiles, then (where lengths tell) those of one
+        for (int pass = 0; pass < 2; ++pass) {
+            const bool one = pass == 1;
+            if (one ? ktiles > 1 && !a.kv_lens : ktiles <= 1) continue;
+            p.zeros = one == (ktiles <= 1);
+            const auto kernel = one ? xattn_dq_kernel<true> : xattn_dq_kernel<false>;
+            if ((e = prepare_kernel(reinterpret_cast<const void*>(kernel), 14 * kChunk)) != cudaSuccess) return e;
+            kernel<<<p.items < num_sms ? p.items : num_sms, kBwdThreads, smem, stream>>>(mq, mg, mk, mv, md, p);
+            if ((e = cudaGetLastError()) != cudaSuccess) return e;
+            ++launches;
+        }
     }
     if (plan.units > 0 && plan.splits > 0) {
         DkvParams p{aq, ag, ak, av, a.dk, a.dv, a.lse, delta, a.kv_lens, partial, a.scale * kLog2e, a.scale, a.H, a.Hkv, a.Lq, a.Lk,

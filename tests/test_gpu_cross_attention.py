@@ -147,6 +147,14 @@ def test_valid_lengths(cuda_ok, lens, Lq):
         assert not dk[b, n:].any() and not dv[b, n:].any()
 
 
+@pytest.mark.parametrize("lens", [[300, 5, 0, 129, 128], [1, 2, 128, 0, 0], [129, 300, 256, 257, 300], [0, 0, 0, 0, 127]])
+def test_samples_of_one_and_more_key_tiles(cuda_ok, lens):
+    """Samples whose states fill one tile of keys beside longer and empty ones."""
+    q, k, v, do = _inputs(5, 150, 300, 4, 2, 72, seed=21)
+    dq = _check(q, k, v, lens, do=do)[2]
+    assert not any(dq[b].any() for b, n in enumerate(lens) if n == 0)
+
+
 @pytest.mark.parametrize("H,Hkv", [(1, 1), (4, 1), (6, 2), (8, 4), (16, 1), (20, 1)])
 @pytest.mark.parametrize("Lq", [1, 4, 140])
 def test_shared_heads(cuda_ok, H, Hkv, Lq):
