@@ -25,8 +25,10 @@ extern "C" {
  * Weights and products are exact (in FP16 with a row's values times a power of
  * two where they span few enough binades, in bf16 otherwise), products are added
  * in FP32, g and the bias are applied in FP32, and y is rounded once.
- * x_bf16    [M, K] bf16, row stride ld_x (ld_x >= K, ld_x % 8 == 0), 16-byte
- *           aligned; 1 <= M <= NVFP4_GEMV_MAX_ROWS (M == 0 is a no-op).
+ * x_bf16    [M, K] bf16, row stride ld_x (ld_x >= K, ld_x % 8 == 0; 0: the M rows
+ *           are one row in memory, as where samples share their conditioning),
+ *           16-byte aligned; 1 <= M <= NVFP4_GEMV_MAX_ROWS (M == 0 is a no-op).
+ *           The stride of a single row is checked as any, and not used.
  * w_format  NVFP4_WEIGHTS_NVFP4: w_codes, w_sf, w_scale as nvfp4_quantize
  *           writes a [N, K] tensor (block 16, s = e4m3, g = *w_scale), K % 64 == 0;
  *           NVFP4_WEIGHTS_MX: w_codes, w_sf as nvfp4_mx_quantize writes them

@@ -572,7 +572,8 @@ def _used_on(stream, *tensors) -> None:
 def gemv_w4a16(x: torch.Tensor, w: NVFP4Tensor | MXTensor, bias: torch.Tensor | None = None,
                out_dtype=torch.bfloat16, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Y = X W^T (+ bias) for at most NVFP4_GEMV_MAX_ROWS rows: X bf16 [M, K]
-    (rows may be strided), W NVFP4 or MX [N, K], bias FP32 [N], Y bf16 or FP32."""
+    (rows may be strided, or one row expanded to M), W NVFP4 or MX [N, K], bias
+    FP32 [N], Y bf16 or FP32."""
     mx = isinstance(w, MXTensor)
     codes, sf, scale, N, K = w.codes, w.sf, None if mx else w.scale, w.rows, w.k
     if x.dtype is not torch.bfloat16 or x.dim() != 2 or x.shape[1] != K:
@@ -583,6 +584,10 @@ def gemv_w4a16(x: torch.Tensor, w: NVFP4Tensor | MXTensor, bias: torch.Tensor | 
         raise ValueError("at most NVFP4_GEMV_MAX_ROWS rows: gemm_w4a16 takes more")
     if step != 1:
         raise ValueError("x must be contiguous along k")
+    if M <= 1:
+        ld = K                                         # never used
+    elif 0 < ld < K:
+        raise ValueError("rows of x must not overlap: their stride is at least w.k, or 0 for one row expanded")
     if bias is not None and (bias.dtype is not torch.float32 or bias.shape != (N,) or not bias.is_contiguous()):
         raise ValueError("bias must be a contiguous FP32 [N]")
     y_dtype = _DT.get(out_dtype if out is None else out.dtype)
@@ -594,7 +599,7 @@ def gemv_w4a16(x: torch.Tensor, w: NVFP4Tensor | MXTensor, bias: torch.Tensor | 
     else:
         y = out
         _require(y.shape == (M, N) and y.is_contiguous(), "out must be a contiguous bf16 or FP32 [M, N]")
-    check(lib().nvfp4_gemv_w4a16(x.data_ptr(), ld if ld > K else K, codes.data_ptr(), sf.data_ptr(),
+    check(lib().nvfp4_gemv_w4a16(x.data_ptr(), ld, codes.data_ptr(), sf.data_ptr(),
                                  None if mx else scale.data_ptr(), NVFP4_WEIGHTS_MX if mx else NVFP4_WEIGHTS_NVFP4,
                                  None if bias is None else bias.data_ptr(), M, N, K, y.data_ptr(), y_dtype,
                                  _stream(stream)), "nvfp4_gemv_w4a16")

@@ -65,7 +65,7 @@ extern "C" {
 nvfp4_status nvfp4_gemv_w4a16(const void* x_bf16, int64_t ld_x, const uint8_t* w_codes, const uint8_t* w_sf,
                               const float* w_scale, int w_format, const float* bias, int64_t M, int64_t N, int64_t K,
                               void* y, int y_dtype, nvfp4_stream_t stream) {
-    if (M < 0 || N <= 0 || K <= 0 || ld_x < K) return NVFP4_ERR_INVALID_ARG;
+    if (M < 0 || N <= 0 || K <= 0 || (ld_x < K && ld_x != 0)) return NVFP4_ERR_INVALID_ARG;
     if (w_format != NVFP4_WEIGHTS_NVFP4 && w_format != NVFP4_WEIGHTS_MX) return NVFP4_ERR_INVALID_ARG;
     if (y_dtype != NVFP4_DTYPE_BF16 && y_dtype != NVFP4_DTYPE_F32) return NVFP4_ERR_INVALID_ARG;
     const bool mx = w_format == NVFP4_WEIGHTS_MX;
