@@ -98,7 +98,9 @@ nvfp4_status nvfp4_rotary(const nvfp4_heads *x, const void *positions, int pos_d
  * kv_lens   nullable device int32 [B]: values below 0 count as 0, above Lk as
  *           Lk.  Keys at or past the length are not read into any result,
  *           whatever their memory holds (NaN and infinities too).  A sample
- *           of length 0 gets out = 0 and lse = -infinity.
+ *           of length 0 gets out = 0 and lse = -infinity.  (A query whose logits
+ *           are -infinity at every valid key gets 0 / 0, out = NaN, and
+ *           lse = -infinity.)
  * scale     finite and > 0 (usually 1 / sqrt(d)).
  * lse       nullable, out: device FP32 [B, H, Lq] contiguous.
  * d % 8 == 0, 8 <= d <= 128; any Lq >= 0, Lk >= 0; B * H * Lq and B * Hkv * Lk

@@ -224,8 +224,9 @@ __device__ __forceinline__ F2 mul2(F2 a, F2 b) {
 
 // 2^x of two values on the FMA pipes, for -inf <= x < 127: x = n + r with |r| <=
 // 1/2, 2^r by the polynomial of degree 5 of least relative error (Remez exchange,
-// 2^-23.7; 2^-22.1 with the roundings of FP32), times 2^n.  Below -126 it is
-// 2^-126; NaN stays NaN.  The hardware exponential does 16 values a cycle and SM,
+// 2^-23.7; 2^-22.1 with the roundings of FP32), times 2^n.  Below -126, at
+// -infinity too, it is 2^-126 (a sum of nothing else has to be told apart by its
+// maximum); NaN stays NaN.  The hardware exponential does 16 values a cycle and SM,
 // and a tile of 128 x 128 takes 1024 cycles of it: a part goes this way.
 __device__ __forceinline__ F2 ex2_fma(F2 x) {
     asm("max.NaN.f32 %0, %0, 0fC2FC0000;" : "+f"(x.x));

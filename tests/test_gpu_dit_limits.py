@@ -23,3 +23,39 @@ def test_gemv_of_one_row_expanded(cuda_ok, fmt, M, N, K):
             y = nv.gemv_w4a16(x, w, out_dtype=dtype)
             assert torch.equal(y, nv.gemv_w4a16(x.contiguous(), w, out_dtype=dtype))
             assert bool((y == y[:1]).all())
+
+
+@pytest.mark.parametrize("Lq", [4, 200])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("Lk", [1, 14, 15, 16, 31, 128, 129, 300])
+def test_row_of_minus_infinity_everywhere(cuda_ok, Lq, d, Lk):
+    """exp(-infinity) over a sum of nothing else is 0 / 0: NaN in both kernels,
+    lse = -infinity, NaN gradients; the other sample does not notice."""
+    g = torch.Generator(device="cuda").manual_seed(Lk)
+    q, k, v, do = (torch.randn(2, n, 2, d, generator=g, device="cuda").bfloat16() for n in (Lq, Lk, Lk, Lq))
+    q[0, ..., 0] = q[0, ..., 0].abs() + 1
+    base, base_lse = nv.cross_attention(q, k, v, return_lse=True)
+    base_grads = nv.cross_attention_backward(do, q, k, v, base, base_lse)
+    k[0, ..., 0] = -float("inf")
+    out, lse = nv.cross_attention(q, k, v, return_lse=True)
+    grads = nv.cross_attention_backward(do, q, k, v, out, lse)
+    assert bool(out[0].isnan().all()) and bool((lse[0] == -float("inf")).all())
+    assert all(bool(t[0].isnan().all()) for t in grads)
+    assert torch.equal(out[1], base[1]) and torch.equal(lse[1], base_lse[1])
+    assert all(torch.equal(t[1], b[1]) for t, b in zip(grads, base_grads))
+
+
+@pytest.mark.parametrize("Lk", [15, 128, 300])
+def test_rows_of_minus_infinity_among_others(cuda_ok, Lk):
+    """Only the rows whose logits are all -infinity become NaN: keys of -infinity
+    in one column meet queries that are 1 there, and queries that are -1 see
+    +infinity, NaN too; a head without such a column keeps its bits."""
+    g = torch.Generator(device="cuda").manual_seed(Lk)
+    q, k, v = (torch.randn(1, n, 2, 64, generator=g, device="cuda").bfloat16() for n in (200, Lk, Lk))
+    base = nv.cross_attention(q, k, v)
+    q[:, :, 0, 0] = torch.where(torch.arange(200, device="cuda") % 3 == 0, -1.0, 1.0).bfloat16()
+    k[:, :, 0, 0] = -float("inf")
+    out, lse = nv.cross_attention(q, k, v, return_lse=True)
+    assert bool(out[:, :, 0].isnan().all()) and torch.equal(out[:, :, 1], base[:, :, 1])
+    up = torch.arange(200, device="cuda") % 3 == 0
+    assert bool((lse[0, 0, ~up] == -float("inf")).all()) and bool(lse[0, 0, up].isnan().all())
