@@ -33,8 +33,9 @@ extern "C" {
  *           writes a [N, K] tensor (block 16, s = e4m3, g = *w_scale), K % 64 == 0;
  *           NVFP4_WEIGHTS_MX: w_codes, w_sf as nvfp4_mx_quantize writes them
  *           (block 32, s = 2^(byte - 127), g = 1, w_scale ignored), K % 128 == 0.
+ *           Either: K <= 2^31 - 128.
  * bias      nullable device FP32 [N].
- * y         [M, N] contiguous in y_dtype (any N >= 1).
+ * y         [M, N] contiguous in y_dtype (1 <= N < 2^31 - 128).
  * The K range is split over the warps of a CTA and the CTAs of a cluster, whose
  * sums are added in a fixed order: the same call gives the same bits.  (How it is
  * split depends on M, N and K: a row's bits may differ between calls of other M.)
@@ -103,8 +104,8 @@ nvfp4_status nvfp4_rotary(const nvfp4_heads *x, const void *positions, int pos_d
  *           lse = -infinity.)
  * scale     finite and > 0 (usually 1 / sqrt(d)).
  * lse       nullable, out: device FP32 [B, H, Lq] contiguous.
- * d % 8 == 0, 8 <= d <= 128; any Lq >= 0, Lk >= 0; B * H * Lq and B * Hkv * Lk
- * below 2^31.
+ * d % 8 == 0, 8 <= d <= 128; 0 <= Lq, Lk <= 2^31 - 128; B * H * (Lq + 1) and
+ * B * Hkv * (Lk + 1) below 2^31.
  * S = q k^T and P v run on the tensor cores with FP32 accumulation, the softmax
  * is FP32, P is rounded to bf16 for the second product.  One kernel on
  * `stream`.

@@ -14,6 +14,7 @@ using namespace nvfp4;
 namespace {
 
 constexpr int64_t kMaxInt = (int64_t)1 << 31;
+constexpr int64_t kMaxTiled = kMaxInt - 128;           // lengths that kernels round up to tiles of 128 in 32 bits
 constexpr int64_t kMaxStride = (int64_t)1 << 37;       // elements: below the 2^40 bytes of a tensor map's stride
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -51,7 +52,7 @@ nvfp4_status check_attention_sizes(int64_t B, int64_t H, int64_t Hkv, int64_t Lq
     if (!(scale > 0.0f) || std::isinf(scale)) return NVFP4_ERR_INVALID_ARG;
     if (H % Hkv != 0) return NVFP4_ERR_INVALID_ARG;
     if (d % 8 != 0 || d > 128) return NVFP4_ERR_UNSUPPORTED_SHAPE;
-    if (B >= kMaxInt || H >= kMaxInt || Lq >= kMaxInt || Lk >= kMaxInt || B * H >= kMaxInt ||
+    if (B >= kMaxInt || H >= kMaxInt || Lq > kMaxTiled || Lk > kMaxTiled || B * H >= kMaxInt ||
         B * H * (Lq + 1) >= kMaxInt || B * Hkv * (Lk + 1) >= kMaxInt)
         return NVFP4_ERR_UNSUPPORTED_SHAPE;
     if (!aligned4(kv_lens)) return NVFP4_ERR_MISALIGNED;
@@ -70,7 +71,7 @@ nvfp4_status nvfp4_gemv_w4a16(const void* x_bf16, int64_t ld_x, const uint8_t* w
     if (y_dtype != NVFP4_DTYPE_BF16 && y_dtype != NVFP4_DTYPE_F32) return NVFP4_ERR_INVALID_ARG;
     const bool mx = w_format == NVFP4_WEIGHTS_MX;
     if (M > NVFP4_GEMV_MAX_ROWS || K % (mx ? 128 : 64) != 0) return NVFP4_ERR_UNSUPPORTED_SHAPE;
-    if (N >= kMaxInt - 128 || K >= kMaxInt || ld_x >= kMaxStride) return NVFP4_ERR_UNSUPPORTED_SHAPE;
+    if (N >= kMaxTiled || K > kMaxTiled || ld_x >= kMaxStride) return NVFP4_ERR_UNSUPPORTED_SHAPE;
     if (M == 0) return NVFP4_OK;                 /* nothing to read or write */
     if (!x_bf16 || !w_codes || !w_sf || (!mx && !w_scale) || !y) return NVFP4_ERR_INVALID_ARG;
     if (!aligned16(x_bf16) || !aligned16(w_codes) || !aligned16(w_sf) || !aligned16(y) || (M > 1 && ld_x % 8 != 0) ||
