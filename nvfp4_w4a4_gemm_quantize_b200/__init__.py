@@ -617,7 +617,7 @@ def _rows16(t: torch.Tensor) -> torch.Tensor:
             s % n == 0 and (s >= t.shape[-1] or (s == 0 and i != 1)) for i, (s, size) in
             enumerate(zip(t.stride()[:-1], t.shape)) if size > 1):
         return t
-    return t.contiguous()
+    return t.clone(memory_format=torch.contiguous_format)      # contiguous() keeps a contiguous tensor where it is
 
 
 def rotary(x: torch.Tensor, positions: torch.Tensor, axes, theta: float = 10000.0, interleaved: bool = True,

@@ -51,3 +51,33 @@ def test_gemv_refuses_rows_that_overlap(recorder, stride):
     with pytest.raises(ValueError, match="overlap"):
         nv.gemv_w4a16(x, _weights("nvfp4"))
     assert not recorder.calls
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("what", ["contiguous", "contiguous, off by one", "padded rows", "rows of 65", "one for all", "tokens shared",
+                                  "head major", "empty"])
+def test_gradients_get_rows_of_16_bytes(dtype, what):
+    """Whatever a gradient's memory looks like, the backward calls get the same
+    values with d contiguous and 16-byte steps, and the tensor itself where it
+    has them already."""
+    B, L, H, d = 2, 5, 3, 64
+    n = B * L * H * d
+    buf = torch.randn(4 * n, dtype=torch.float32).to(dtype)
+    assert buf.data_ptr() % 16 == 0
+    t, kept = {
+        "contiguous": (buf[:n].view(B, L, H, d), True),
+        "contiguous, off by one": (buf[1:n + 1].view(B, L, H, d), False),
+        "padded rows": (buf.as_strided((B, L, H, d), (L * H * 72, H * 72, 72, 1)), True),
+        "rows of 65": (buf.as_strided((B, L, H, d), (L * H * 65, H * 65, 65, 1)), False),
+        "one for all": (buf[:1].view(1, 1, 1, 1).expand(B, L, H, d), False),
+        "tokens shared": (buf[:d].view(1, 1, 1, d).expand(B, L, H, d), False),
+        "head major": (buf[:n].view(B, H, L, d).transpose(1, 2), True),
+        "empty": (buf[1:1].view(B, 0, H, d), None),
+    }[what]
+    r = nv._rows16(t)
+    assert r.shape == t.shape and r.dtype == dtype and torch.equal(r, t)
+    assert r.stride(3) == 1 and r.data_ptr() % 16 == 0
+    step = 16 // t.element_size()
+    assert all(s % step == 0 for s in r.stride()[:3])
+    if kept is not None:
+        assert (r is t) == kept

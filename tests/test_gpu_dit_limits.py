@@ -59,3 +59,20 @@ def test_rows_of_minus_infinity_among_others(cuda_ok, Lk):
     assert bool(out[:, :, 0].isnan().all()) and torch.equal(out[:, :, 1], base[:, :, 1])
     up = torch.arange(200, device="cuda") % 3 == 0
     assert bool((lse[0, 0, ~up] == -float("inf")).all()) and bool(lse[0, 0, up].isnan().all())
+
+
+@pytest.mark.parametrize("Lq", [3, 150])
+def test_gradients_off_a_16_byte_boundary(cuda_ok, Lq):
+    """A contiguous gradient that starts two bytes into its storage."""
+    g = torch.Generator(device="cuda").manual_seed(Lq)
+    q, k, v, do = (torch.randn(2, n, 2, 64, generator=g, device="cuda").bfloat16() for n in (Lq, 40, 40, Lq))
+    off = torch.empty(do.numel() + 1, device="cuda", dtype=torch.bfloat16)[1:].view_as(do).copy_(do)
+    assert off.is_contiguous() and off.data_ptr() % 16 == 2
+    leaves = [t.requires_grad_() for t in (q, k, v)]
+    want = torch.autograd.grad(nv.CrossAttention.apply(*leaves), leaves, do)
+    got = torch.autograd.grad(nv.CrossAttention.apply(*leaves), leaves, off)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    at = torch.arange(Lq, device="cuda", dtype=torch.int32)[:, None]
+    want = torch.autograd.grad(nv.RotaryEmbedding.apply(q, at, (64,)), q, do)[0]
+    got = torch.autograd.grad(nv.RotaryEmbedding.apply(q, at, (64,)), q, off)[0]
+    assert torch.equal(got, want)
