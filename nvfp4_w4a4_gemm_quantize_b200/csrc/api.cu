@@ -74,17 +74,30 @@ struct DevInfo {
 };
 static DevInfo g_dev[64];
 
+typedef CUresult (*CtxGetCurrentFn)(CUcontext*);
+
+static bool has_context() {
+    static CtxGetCurrentFn fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPoint("cuCtxGetCurrent", &p, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<CtxGetCurrentFn>(p);
+    });
+    CUcontext c = nullptr;
+    return fn && fn(&c) == CUDA_SUCCESS && c != nullptr;
+}
+
 nvfp4_status device_ok(int* sms) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return NVFP4_ERR_CUDA;
     if (dev < 0 || dev >= 64) return NVFP4_ERR_UNSUPPORTED_DEVICE;
-    // a thread that made no CUDA call yet (an autograd worker) has no current
-    // context, which encoding a tensor map needs
-    static thread_local int bound = -1;
-    if (bound != dev) {
-        if (cudaSetDevice(dev) != cudaSuccess) return NVFP4_ERR_CUDA;
-        bound = dev;
-    }
+    // A thread that made no CUDA call yet (an autograd worker) has no current
+    // context, which encoding a tensor map needs.  A context that is current,
+    // the caller's own included, stays.
+    if (!has_context() && cudaSetDevice(dev) != cudaSuccess) return NVFP4_ERR_CUDA;
     DevInfo& d = g_dev[dev];
     if (d.checked == 0) {
         int major = 0, minor = 0, n = 0;

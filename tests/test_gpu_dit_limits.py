@@ -1,5 +1,8 @@
 """Calls at the edges of what include/nvfp4_dit.h allows: operands that share
 memory, values that are not finite, other streams and contexts."""
+import ctypes
+import threading
+
 import pytest
 import torch
 
@@ -76,3 +79,27 @@ def test_gradients_off_a_16_byte_boundary(cuda_ok, Lq):
     want = torch.autograd.grad(nv.RotaryEmbedding.apply(q, at, (64,)), q, do)[0]
     got = torch.autograd.grad(nv.RotaryEmbedding.apply(q, at, (64,)), q, off)[0]
     assert torch.equal(got, want)
+
+
+def test_the_callers_context_stays_current(cuda_ok):
+    """A thread with a context of its own still has it after a call (one that
+    asks for the device and has nothing to launch)."""
+    torch.zeros(1, device="cuda")
+    cuda = ctypes.CDLL("libcuda.so.1")
+    primary, mine, after = ctypes.c_void_p(), ctypes.c_void_p(), ctypes.c_void_p()
+    assert cuda.cuCtxGetCurrent(ctypes.byref(primary)) == 0 and primary.value
+    assert cuda.cuCtxCreate_v2(ctypes.byref(mine), 0, 0) == 0               # becomes current here
+    assert cuda.cuCtxSetCurrent(primary) == 0
+    results = []
+
+    def work():
+        results.append(cuda.cuCtxSetCurrent(mine))
+        results.append(nv.lib().nvfp4_dequantize(None, None, None, 0, 64, None, nv.NVFP4_DTYPE_BF16, None))
+        results.append(cuda.cuCtxGetCurrent(ctypes.byref(after)))
+
+    t = threading.Thread(target=work)
+    t.start()
+    t.join()
+    assert cuda.cuCtxDestroy_v2(mine) == 0
+    assert cuda.cuCtxSetCurrent(primary) == 0
+    assert results == [0, 0, 0] and after.value == mine.value
