@@ -147,7 +147,8 @@ __device__ __forceinline__ void mma_first(float (&c)[4], uint32_t a0, uint32_t a
 
 // Scales of a lane's 32 k of one feature.
 //   NVFP4: two blocks; e4m3 times 2^119 as bf16 pairs.  A byte moved to bf16's
-//     exponent and mantissa reads as the scale times 2^-120 (subnormals too).
+//     exponent and mantissa reads as the scale times 2^-120 (subnormals too);
+//     0x7F, which would read as 480, is set to NaN.
 //   MX: one block; 2^(byte - 1), or 2^127 and the rest in `over`.
 template <bool MX>
 struct Scales {
@@ -163,7 +164,7 @@ struct Scales {
             const uint32_t h = word >> (16 * (t & 1));
             uint32_t v;
             asm("prmt.b32 %0, %1, 0, 0x4140;" : "=r"(v) : "r"(h & 0x7F7Fu));
-            v = mul_bf16x2(mul_bf16x2(v << 4, kTwo120), kTwo119);
+            v = mul_bf16x2(mul_bf16x2(v << 4, kTwo120), kTwo119) | (__vcmpeq2(v, 0x007F007Fu) & 0x7FFF7FFFu);
             asm("prmt.b32 %0, %1, 0, 0x1010;" : "=r"(s[0]) : "r"(v));
             asm("prmt.b32 %0, %1, 0, 0x3232;" : "=r"(s[1]) : "r"(v));
         }

@@ -103,3 +103,27 @@ def test_the_callers_context_stays_current(cuda_ok):
     assert cuda.cuCtxDestroy_v2(mine) == 0
     assert cuda.cuCtxSetCurrent(primary) == 0
     assert results == [0, 0, 0] and after.value == mine.value
+
+
+@pytest.mark.parametrize("M", [1, 5, 16])
+@pytest.mark.parametrize("spread", [0, 100])
+@pytest.mark.parametrize("byte", [0x7F, 0xFF])
+def test_gemv_of_a_nan_scale(cuda_ok, M, spread, byte):
+    """E4M3's NaN makes its feature NaN in every row of x, be x's values close
+    together or 2^100 apart (which are decoded in different ways), as
+    dequantize() has it; the other features keep their bits."""
+    N, K = 200, 640
+    w = nv.quantize(synth.random_bf16((N, K), seed=1, scale=0.02).cuda())
+    x = synth.random_bf16((M, K), seed=2).cuda()
+    x[:, 3] *= 2.0 ** -spread
+    base = nv.gemv_w4a16(x, w, out_dtype=torch.float32)
+    features = torch.tensor([0, 77, 130, 199])
+    for i, n in enumerate(features.tolist()):
+        c = 7 * i + 2                                       # one block of 16 along k
+        w.sf[(n // 128 * (K // 64) + c // 4) * 512 + n % 32 * 16 + n % 128 // 32 * 4 + c % 4] = byte
+    bad = torch.zeros(N, dtype=torch.bool)
+    bad[features] = True
+    values = nv.dequantize(w, torch.float32)
+    assert torch.equal(values.isnan().any(1).cpu(), bad)
+    y = nv.gemv_w4a16(x, w, out_dtype=torch.float32)
+    assert bool(y[:, bad].isnan().all()) and torch.equal(y[:, ~bad], base[:, ~bad])
