@@ -5,7 +5,8 @@ marshals torch tensors into pointers and sizes and calls the library of the
 same name; all arithmetic runs in the CUDA kernels.  torch supplies device
 memory and streams.  Every tensor must live on the current CUDA device (the
 library launches there; nothing here switches devices), and the default stream
-argument is that device's current torch stream.
+argument is that device's current torch stream.  On another stream the caller
+sees to it that inputs are ready there and that results are waited for.
 
 Low-level (same names and argument order as the C calls):
     nvfp4_sf_bytes, nvfp4_quantize_workspace_bytes, nvfp4_quantize,
@@ -560,13 +561,24 @@ def _on_device(*tensors) -> None:
             raise ValueError(f"tensor on {t.device}: the call runs on the current CUDA device")
 
 
-def _used_on(stream, *tensors) -> None:
-    """Tensors a call allocated (on the current stream) stay unrecycled until
-    the other stream the call runs on has passed."""
+def _empty_on(stream, shape, dtype, device, returned=True) -> torch.Tensor:
+    """A tensor that a call writes on ``stream``, from that stream's own memory:
+    memory that the current stream has freed may still be in use there.  What
+    is ``returned`` may be used on the current stream (once that has waited for
+    the call) and is not recycled before it has passed."""
+    here = torch.cuda.current_stream()
     s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
-    if s != torch.cuda.current_stream():
-        for t in tensors:
-            t.record_stream(s)
+    with torch.cuda.stream(s):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if returned and s != here:
+        t.record_stream(here)
+    return t
+
+
+def _empty(stream, shape, dtype, device) -> torch.Tensor:
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    return _empty_on(stream, shape, dtype, device)
 
 
 def gemv_w4a16(x: torch.Tensor, w: NVFP4Tensor | MXTensor, bias: torch.Tensor | None = None,
@@ -595,7 +607,7 @@ def gemv_w4a16(x: torch.Tensor, w: NVFP4Tensor | MXTensor, bias: torch.Tensor | 
         raise ValueError("out must be a contiguous bf16 or FP32 [M, N]")
     _on_device(x, codes, sf, scale, bias, out)
     if out is None:
-        y = torch.empty(M, N, dtype=out_dtype, device=x.device)
+        y = _empty(stream, (M, N), out_dtype, x.device)
     else:
         y = out
         _require(y.shape == (M, N) and y.is_contiguous(), "out must be a contiguous bf16 or FP32 [M, N]")
@@ -603,8 +615,6 @@ def gemv_w4a16(x: torch.Tensor, w: NVFP4Tensor | MXTensor, bias: torch.Tensor | 
                                  None if mx else scale.data_ptr(), NVFP4_WEIGHTS_MX if mx else NVFP4_WEIGHTS_NVFP4,
                                  None if bias is None else bias.data_ptr(), M, N, K, y.data_ptr(), y_dtype,
                                  _stream(stream)), "nvfp4_gemv_w4a16")
-    if out is None and stream is not None:
-        _used_on(stream, y)
     return y
 
 
@@ -645,7 +655,7 @@ def rotary(x: torch.Tensor, positions: torch.Tensor, axes, theta: float = 10000.
         raise ValueError("positions must be contiguous along the axes")
     if out is None:
         _on_device(x, positions)
-        y = torch.empty(B, L, H, d, dtype=dt, device=x.device)
+        y = _empty(stream, (B, L, H, d), dt, x.device)
         to = _new_heads(y, L, H, d)
     else:
         y = out
@@ -657,8 +667,6 @@ def rotary(x: torch.Tensor, positions: torch.Tensor, axes, theta: float = 10000.
                              NVFP4_POSITION_I32 if pd is torch.int32 else NVFP4_POSITION_F32, pt[0] if per_sample else 0,
                              pt[-2], _ints(axes), len(axes), float(theta), B, L, H, d, dtype, flags, to, _stream(stream)),
           "nvfp4_rotary")
-    if out is None and stream is not None:
-        _used_on(stream, y)
     return y
 
 
@@ -705,20 +713,18 @@ def cross_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, kv_lens: 
     (B, H, Hkv, Lq, Lk, d), hq, hk, hv = _attention_operands(q, k, v, kv_lens)
     if out is None:
         _on_device(q, k, v, kv_lens, dev_status)
-        o = torch.empty(B, Lq, H, d, dtype=torch.bfloat16, device=q.device)
+        o = _empty(stream, (B, Lq, H, d), torch.bfloat16, q.device)
         to = _new_heads(o, Lq, H, d)
     else:
         o = out
         _require(o.dtype == torch.bfloat16 and o.shape == q.shape and o.stride(3) == 1, "out must be a bf16 tensor of q's shape")
         _on_device(q, k, v, kv_lens, o, dev_status)
         to = _heads(o)
-    lse = torch.empty(B, H, Lq, dtype=torch.float32, device=q.device) if return_lse else None
+    lse = _empty(stream, (B, H, Lq), torch.float32, q.device) if return_lse else None
     check(lib().nvfp4_cross_attention(hq, hk, hv, None if kv_lens is None else kv_lens.data_ptr(),
                                       d ** -0.5 if scale is None else float(scale), B, H, Hkv, Lq, Lk, d, to,
                                       None if lse is None else lse.data_ptr(), _ptr(dev_status), _stream(stream)),
           "nvfp4_cross_attention")
-    if stream is not None:
-        _used_on(stream, *([o] if out is None else []), *([lse] if return_lse else []))
     return (o, lse) if return_lse else o
 
 
@@ -736,25 +742,24 @@ def cross_attention_backward(grad_out: torch.Tensor, q: torch.Tensor, k: torch.T
         raise ValueError("grad_out and out must be bf16 tensors of q's shape, d contiguous")
     if lse.dtype is not torch.float32 or lse.shape != (B, H, Lq) or not lse.is_contiguous():
         raise ValueError("lse must be a contiguous FP32 [B, H, Lq]")
+    _on_device(grad_out, q, k, v, out, lse, kv_lens, workspace, dev_status)
     if workspace is None:
         bytes_ = nvfp4_cross_attention_backward_workspace_bytes(*sizes)
-        ws = torch.empty(bytes_, dtype=torch.uint8, device=device)
+        ws = (torch.empty(bytes_, dtype=torch.uint8, device=device) if stream is None else
+              _empty_on(stream, bytes_, torch.uint8, device, returned=False))
     else:
         ws = workspace
         _require(ws.is_contiguous(), "workspace must be contiguous")
         bytes_ = ws.numel() * ws.element_size()
-    dq = torch.empty(B, Lq, H, d, dtype=bf16, device=device)
-    dk = torch.empty(B, Lk, Hkv, d, dtype=bf16, device=device)
-    dv = torch.empty(B, Lk, Hkv, d, dtype=bf16, device=device)
-    _on_device(grad_out, q, k, v, out, lse, kv_lens, ws, dev_status)
+    dq = _empty(stream, (B, Lq, H, d), bf16, device)
+    dk = _empty(stream, (B, Lk, Hkv, d), bf16, device)
+    dv = _empty(stream, (B, Lk, Hkv, d), bf16, device)
     check(lib().nvfp4_cross_attention_backward(
         _PACK_HEADS(grad_out.data_ptr(), gt[0], gt[1], gt[2]), hq, hk, hv, _PACK_HEADS(out.data_ptr(), ot[0], ot[1], ot[2]),
         lse.data_ptr(),
         None if kv_lens is None else kv_lens.data_ptr(), d ** -0.5 if scale is None else float(scale), B, H, Hkv, Lq, Lk, d,
         _new_heads(dq, Lq, H, d), _new_heads(dk, Lk, Hkv, d), _new_heads(dv, Lk, Hkv, d), ws.data_ptr(), bytes_,
         _ptr(dev_status), _stream(stream)), "nvfp4_cross_attention_backward")
-    if stream is not None:
-        _used_on(stream, dq, dk, dv, *((ws,) if workspace is None else ()))
     return dq, dk, dv
 
 

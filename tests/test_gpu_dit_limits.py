@@ -127,3 +127,68 @@ def test_gemv_of_a_nan_scale(cuda_ok, M, spread, byte):
     assert torch.equal(values.isnan().any(1).cpu(), bad)
     y = nv.gemv_w4a16(x, w, out_dtype=torch.float32)
     assert bool(y[:, bad].isnan().all()) and torch.equal(y[:, ~bad], base[:, ~bad])
+
+
+def _calls_on_a_stream():
+    """name: (inputs' maker, call of them on a stream)"""
+    def gemv():
+        w = nv.quantize(synth.random_bf16((1280, 256), seed=3, scale=0.02).cuda())
+        x = synth.random_bf16((4, 256), seed=4).cuda()
+        return lambda s: [nv.gemv_w4a16(x, w, out_dtype=torch.float32, stream=s)]
+
+    def rotary():
+        x = torch.randn(1, 90, 4, 64, device="cuda").bfloat16()
+        at = torch.arange(90, device="cuda", dtype=torch.int32)[:, None]
+        return lambda s: [nv.rotary(x, at, (64,), stream=s)]
+
+    def attention(Lq):
+        q, k, v, do = (torch.randn(2, n, 4, 64, device="cuda").bfloat16() for n in (Lq, 300, 300, Lq))
+        out, lse = nv.cross_attention(q, k, v, return_lse=True)
+        return lambda s: [*nv.cross_attention(q, k, v, return_lse=True, stream=s),
+                          *nv.cross_attention_backward(do, q, k, v, out, lse, stream=s)]
+
+    return {"gemv": gemv, "rotary": rotary, "few queries": lambda: attention(3), "queries": lambda: attention(200)}
+
+
+@pytest.mark.parametrize("name", ["gemv", "rotary", "few queries", "queries"])
+@pytest.mark.parametrize("as_int", [False, True])
+def test_a_call_on_another_stream_takes_no_memory_still_in_use(cuda_ok, name, as_int):
+    """The current stream has freed blocks of just the outputs' sizes, which
+    work that it has still to do will write: the call on the other stream, which
+    does not wait for that, neither gets nor disturbs them."""
+    call = _calls_on_a_stream()[name]()
+    want = call(None)
+    sizes = [t.numel() * t.element_size() for t in want]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    freed = [torch.empty(n, dtype=torch.uint8, device="cuda") for n in sizes for _ in range(4)]
+    kept = torch.zeros(1 << 20, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    torch.cuda._sleep(100_000_000)                       # about 50 ms
+    for t in freed:
+        t.fill_(0x5A)
+    del t, freed
+    got = call(side.cuda_stream if as_int else side)
+    kept.copy_(torch.full_like(kept, 3))
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert bool((kept == 3).all())
+
+
+def test_results_of_another_stream_outlive_their_use_here(cuda_ok):
+    """A result that the current stream still reads is not recycled by the next
+    call on the stream that made it."""
+    x, at = torch.randn(1, 90, 4, 64, device="cuda"), torch.arange(90, device="cuda", dtype=torch.int32)[:, None]
+    other = torch.randn(1, 90, 4, 64, device="cuda")
+    want = nv.rotary(x, at, (64,))
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    y = nv.rotary(x, at, (64,), stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda._sleep(100_000_000)
+    copy = y.clone()                                     # queued behind the sleep
+    del y
+    for _ in range(4):
+        nv.rotary(other, at, (64,), stream=side)
+    torch.cuda.synchronize()
+    assert torch.equal(copy, want)
