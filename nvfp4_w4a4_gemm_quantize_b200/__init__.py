@@ -671,21 +671,23 @@ def rotary(x: torch.Tensor, positions: torch.Tensor, axes, theta: float = 10000.
 
 
 class RotaryEmbedding(torch.autograd.Function):
-    """Autograd wrapper of rotary(): the backward pass turns the gradient back.
-    Positions get no gradient.  As for any torch operator, a backward pass is
-    captured into a CUDA graph from leaves of the capture's own (x.detach()
-    .requires_grad_()): an eager graph of the same leaves invalidates it."""
+    """Autograd wrapper of rotary(): the backward pass turns the gradient back,
+    and can be differentiated again (the map is linear).  Positions get no
+    gradient.  As for any torch operator, a backward pass is captured into a
+    CUDA graph from leaves of the capture's own (x.detach().requires_grad_()):
+    an eager graph of the same leaves invalidates it."""
 
     @staticmethod
-    def forward(ctx, x, positions, axes, theta=10000.0, interleaved=True):
+    def forward(ctx, x, positions, axes, theta=10000.0, interleaved=True, inverse=False):
         ctx.save_for_backward(positions)
-        ctx.how = (axes, theta, interleaved)
-        return rotary(x, positions, axes, theta, interleaved)
+        ctx.how = (axes, theta, interleaved, not inverse)
+        return rotary(x, positions, axes, theta, interleaved, inverse)
 
     @staticmethod
     def backward(ctx, grad):
         (positions,) = ctx.saved_tensors
-        return rotary(_rows16(grad), positions, *ctx.how, inverse=True), None, None, None, None
+        turn = RotaryEmbedding.apply if torch.is_grad_enabled() else rotary          # create_graph
+        return turn(_rows16(grad), positions, *ctx.how), None, None, None, None, None
 
 
 def _attention_operands(q, k, v, kv_lens):
@@ -763,9 +765,23 @@ def cross_attention_backward(grad_out: torch.Tensor, q: torch.Tensor, k: torch.T
     return dq, dk, dv
 
 
+class _CrossAttentionGradients(torch.autograd.Function):
+    """The backward pass of CrossAttention under create_graph: its gradients
+    depend on its inputs, but how is not known here."""
+
+    @staticmethod
+    def forward(ctx, *args):
+        return cross_attention_backward(*args)
+
+    @staticmethod
+    def backward(ctx, *grads):
+        raise RuntimeError("CrossAttention has no second derivative")
+
+
 class CrossAttention(torch.autograd.Function):
     """Autograd wrapper of cross_attention() and cross_attention_backward():
-    gradients of q, k and v.  Captured into a CUDA graph as RotaryEmbedding is."""
+    gradients of q, k and v; a second derivative through it is refused.
+    Captured into a CUDA graph as RotaryEmbedding is."""
 
     @staticmethod
     def forward(ctx, q, k, v, kv_lens=None, scale=None):
@@ -777,4 +793,5 @@ class CrossAttention(torch.autograd.Function):
     @staticmethod
     def backward(ctx, grad):
         q, k, v, out, lse, kv_lens = ctx.saved_tensors
-        return (*cross_attention_backward(_rows16(grad), q, k, v, out, lse, kv_lens, ctx.scale), None, None)
+        gradients = _CrossAttentionGradients.apply if torch.is_grad_enabled() else cross_attention_backward
+        return (*gradients(_rows16(grad), q, k, v, out, lse, kv_lens, ctx.scale), None, None)

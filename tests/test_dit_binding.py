@@ -81,3 +81,69 @@ def test_gradients_get_rows_of_16_bytes(dtype, what):
     assert all(s % step == 0 for s in r.stride()[:3])
     if kept is not None:
         assert (r is t) == kept
+
+
+def _turn(x, positions, axes, theta=10000.0, interleaved=True, inverse=False, **kw):
+    """rotary() of neighbouring pairs in elementary operations."""
+    angle = torch.cat([positions[:, a, None].double() * theta ** (-torch.arange(0, w, 2).double() / w)
+                       for a, w in enumerate(axes) if w], 1)[:, None] * (-1 if inverse else 1)
+    u, v = x.double()[..., 0::2], x.double()[..., 1::2]
+    c, s = torch.cos(angle), torch.sin(angle)
+    return torch.stack([u * c - v * s, u * s + v * c], -1).flatten(-2).to(x.dtype)
+
+
+def test_rotary_can_be_differentiated_twice(monkeypatch):
+    """The gradient under create_graph carries its graph: second derivatives are
+    those of the elementary operations, also where the loss has other paths."""
+    monkeypatch.setattr(nv, "rotary", lambda *a, **kw: _turn(*a, **kw).detach())
+    g = torch.Generator().manual_seed(1)
+    at = torch.arange(5)[:, None]
+    x0, w0 = (torch.randn(2, 5, 3, 8, generator=g) for _ in range(2))
+
+    def second(turn):
+        x, w = x0.clone().requires_grad_(), w0.clone().requires_grad_()
+        y = turn(x)
+        (dx,) = torch.autograd.grad((y * w).pow(2).sum() + x.pow(3).sum(), x, create_graph=True)
+        return (dx.detach(), *torch.autograd.grad(dx.pow(2).sum(), (x, w)))
+
+    want = second(lambda x: _turn(x, at, (8,)))
+    for how in (lambda x: nv.RotaryEmbedding.apply(x, at, (8,)), lambda x: nv.RotaryEmbedding.apply(x, at, (8,), 10000.0, True, False)):
+        for a, b in zip(second(how), want):
+            assert torch.allclose(a, b, rtol=1e-5, atol=1e-5 * float(b.abs().max()))
+    # without create_graph: the plain call, no graph
+    x = x0.clone().requires_grad_()
+    (dx,) = torch.autograd.grad(nv.RotaryEmbedding.apply(x, at, (8,), 10000.0, True, True), x, w0)
+    assert not dx.requires_grad and torch.allclose(dx, _turn(w0, at, (8,)), rtol=1e-5, atol=1e-5)
+
+
+def _attention(q, k, v, kv_lens=None, scale=None, return_lse=False, **kw):
+    """cross_attention() of one head per key head, all keys."""
+    s = torch.einsum("blhd,bmhd->bhlm", q, k) * (q.shape[3] ** -0.5 if scale is None else scale)
+    out = torch.einsum("bhlm,bmhd->blhd", torch.softmax(s, 3), v)
+    return (out, torch.logsumexp(s, 3)) if return_lse else out
+
+
+def _attention_backward(do, q, k, v, out, lse, kv_lens=None, scale=None, **kw):
+    with torch.enable_grad():
+        leaves = [t.detach().requires_grad_() for t in (q, k, v)]
+        return torch.autograd.grad(_attention(*leaves, None, scale), leaves, do.detach())
+
+
+def test_attention_refuses_second_derivatives(monkeypatch):
+    """First derivatives under create_graph are as without; a second one through
+    the attention raises, instead of leaving its terms out beside other paths."""
+    monkeypatch.setattr(nv, "cross_attention", lambda *a, **kw: tuple(t.detach() for t in _attention(*a, **kw)))
+    monkeypatch.setattr(nv, "cross_attention_backward", _attention_backward)
+    g = torch.Generator().manual_seed(2)
+    leaves = [torch.randn(2, n, 3, 8, generator=g).requires_grad_() for n in (4, 6, 6)]
+    want = torch.autograd.grad(nv.CrossAttention.apply(*leaves).sum(), leaves)
+    assert not any(t.requires_grad for t in want)
+    for loss in (lambda out: out.sum(), lambda out: out.pow(2).sum()):
+        plain = torch.autograd.grad(loss(nv.CrossAttention.apply(*leaves)), leaves)
+        grads = torch.autograd.grad(loss(nv.CrossAttention.apply(*leaves)), leaves, create_graph=True)
+        assert all(torch.equal(a, b) for a, b in zip(grads, plain))
+        # each beside another path to q
+        for i in range(3):
+            with pytest.raises(RuntimeError, match="second derivative"):
+                torch.autograd.grad(grads[i].pow(2).sum() + leaves[0].pow(2).sum(), leaves[0])
+            grads = torch.autograd.grad(loss(nv.CrossAttention.apply(*leaves)), leaves, create_graph=True)

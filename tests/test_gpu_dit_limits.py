@@ -192,3 +192,25 @@ def test_results_of_another_stream_outlive_their_use_here(cuda_ok):
         nv.rotary(other, at, (64,), stream=side)
     torch.cuda.synchronize()
     assert torch.equal(copy, want)
+
+
+def test_second_derivatives(cuda_ok):
+    """Of rotary positions: z = sum x . turn(w), so its gradient of w is the
+    turned-back x, whose product with a direction has that direction, turned, as
+    its gradient of x.  Of attention: refused."""
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x, w, h = (torch.randn(2, 30, 4, 64, generator=g, device="cuda") for _ in range(3))
+    at = torch.arange(30, device="cuda", dtype=torch.int32)[:, None]
+    for interleaved in (True, False):
+        xs, ws = x.clone().requires_grad_(), w.clone().requires_grad_()
+        z = (xs * nv.RotaryEmbedding.apply(ws, at, (64,), 10000.0, interleaved)).sum()
+        (dw,) = torch.autograd.grad(z, ws, create_graph=True)
+        assert torch.equal(dw, nv.rotary(x, at, (64,), interleaved=interleaved, inverse=True))
+        (dx,) = torch.autograd.grad((dw * h).sum(), xs)
+        assert torch.equal(dx, nv.rotary(h, at, (64,), interleaved=interleaved))
+    q, k, v = (torch.randn(1, n, 2, 64, generator=g, device="cuda").bfloat16().requires_grad_() for n in (20, 30, 30))
+    plain = torch.autograd.grad(nv.CrossAttention.apply(q, k, v).sum(), (q, k, v))
+    grads = torch.autograd.grad(nv.CrossAttention.apply(q, k, v).sum(), (q, k, v), create_graph=True)
+    assert all(torch.equal(a, b) for a, b in zip(grads, plain))
+    with pytest.raises(RuntimeError, match="second derivative"):
+        torch.autograd.grad(grads[1].float().pow(2).sum() + q.float().pow(2).sum(), q)
