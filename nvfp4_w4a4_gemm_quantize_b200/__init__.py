@@ -770,8 +770,8 @@ class _CrossAttentionGradients(torch.autograd.Function):
     depend on its inputs, but how is not known here."""
 
     @staticmethod
-    def forward(ctx, *args):
-        return cross_attention_backward(*args)
+    def forward(ctx, dev_status, *args):
+        return cross_attention_backward(*args, dev_status=dev_status)
 
     @staticmethod
     def backward(ctx, *grads):
@@ -781,17 +781,22 @@ class _CrossAttentionGradients(torch.autograd.Function):
 class CrossAttention(torch.autograd.Function):
     """Autograd wrapper of cross_attention() and cross_attention_backward():
     gradients of q, k and v; a second derivative through it is refused.
-    Captured into a CUDA graph as RotaryEmbedding is."""
+    ``dev_status`` (a zeroed device int32, as for the two calls) is how a pass,
+    forward or backward, tells that a wait in a kernel ran out and its results
+    are incomplete: a training loop that can act on it passes one and looks at it
+    where it looks at its loss.  Captured into a CUDA graph as RotaryEmbedding is."""
 
     @staticmethod
-    def forward(ctx, q, k, v, kv_lens=None, scale=None):
-        out, lse = cross_attention(q, k, v, kv_lens, scale, return_lse=True)
+    def forward(ctx, q, k, v, kv_lens=None, scale=None, dev_status=None):
+        out, lse = cross_attention(q, k, v, kv_lens, scale, return_lse=True, dev_status=dev_status)
         ctx.save_for_backward(q, k, v, out, lse, kv_lens)
-        ctx.scale = scale
+        ctx.scale, ctx.dev_status = scale, dev_status
         return out
 
     @staticmethod
     def backward(ctx, grad):
         q, k, v, out, lse, kv_lens = ctx.saved_tensors
-        gradients = _CrossAttentionGradients.apply if torch.is_grad_enabled() else cross_attention_backward
-        return (*gradients(_rows16(grad), q, k, v, out, lse, kv_lens, ctx.scale), None, None)
+        args = (_rows16(grad), q, k, v, out, lse, kv_lens, ctx.scale)
+        if torch.is_grad_enabled():                            # create_graph
+            return (*_CrossAttentionGradients.apply(ctx.dev_status, *args), None, None, None)
+        return (*cross_attention_backward(*args, dev_status=ctx.dev_status), None, None, None)

@@ -147,3 +147,29 @@ def test_attention_refuses_second_derivatives(monkeypatch):
             with pytest.raises(RuntimeError, match="second derivative"):
                 torch.autograd.grad(grads[i].pow(2).sum() + leaves[0].pow(2).sum(), leaves[0])
             grads = torch.autograd.grad(loss(nv.CrossAttention.apply(*leaves)), leaves, create_graph=True)
+
+
+@pytest.mark.parametrize("create_graph", [False, True])
+def test_attention_passes_its_status_to_both_passes(monkeypatch, create_graph):
+    """dev_status of CrossAttention.apply is that of the forward and of the
+    backward call; without one there is none."""
+    seen = []
+
+    def forward(q, k, v, kv_lens=None, scale=None, out=None, return_lse=False, dev_status=None, stream=None):
+        seen.append(("forward", scale, dev_status))
+        return torch.zeros_like(q), torch.zeros(1, 2, 4)
+
+    def backward(do, q, k, v, out, lse, kv_lens=None, scale=None, workspace=None, dev_status=None, stream=None):
+        assert workspace is None and stream is None
+        seen.append(("backward", scale, dev_status))
+        return torch.zeros_like(q), torch.zeros_like(k), torch.zeros_like(v)
+
+    monkeypatch.setattr(nv, "cross_attention", forward)
+    monkeypatch.setattr(nv, "cross_attention_backward", backward)
+    q, k, v = (torch.zeros(1, n, 2, 8, requires_grad=True) for n in (4, 6, 6))
+    status = torch.zeros(1, dtype=torch.int32)
+    for args, want in (((None, 0.5, status), (0.5, status)), ((None, 0.5), (0.5, None)), ((), (None, None))):
+        seen.clear()
+        torch.autograd.grad(nv.CrossAttention.apply(q, k, v, *args).sum(), (q, k, v), create_graph=create_graph)
+        assert [s[0] for s in seen] == ["forward", "backward"]
+        assert all(s[1] == want[0] and s[2] is want[1] for s in seen)

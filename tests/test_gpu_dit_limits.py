@@ -214,3 +214,17 @@ def test_second_derivatives(cuda_ok):
     assert all(torch.equal(a, b) for a, b in zip(grads, plain))
     with pytest.raises(RuntimeError, match="second derivative"):
         torch.autograd.grad(grads[1].float().pow(2).sum() + q.float().pow(2).sum(), q)
+
+
+def test_training_step_with_a_status(cuda_ok):
+    """The status reaches both passes (it stays 0 where no wait ran out), and
+    changes nothing else."""
+    g = torch.Generator(device="cuda").manual_seed(4)
+    q, k, v = (torch.randn(2, n, 2, 64, generator=g, device="cuda").bfloat16().requires_grad_() for n in (150, 200, 200))
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    plain = nv.CrossAttention.apply(q, k, v)
+    out = nv.CrossAttention.apply(q, k, v, None, None, status)
+    grads = [torch.autograd.grad(o.sum(), (q, k, v)) for o in (plain, out)]
+    assert torch.equal(out, plain) and all(torch.equal(a, b) for a, b in zip(*grads)) and int(status.item()) == 0
+    with pytest.raises(ValueError):
+        nv.CrossAttention.apply(q, k, v, None, None, status.cpu())
