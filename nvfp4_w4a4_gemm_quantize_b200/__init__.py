@@ -561,7 +561,7 @@ def _on_device(*tensors) -> None:
             raise ValueError(f"tensor on {t.device}: the call runs on the current CUDA device")
 
 
-def _empty_on(stream, shape, dtype, device, returned=True) -> torch.Tensor:
+def _empty_on(stream, dtype, device, *shape, returned=True) -> torch.Tensor:
     """A tensor that a call writes on ``stream``, from that stream's own memory:
     memory that the current stream has freed may still be in use there.  What
     is ``returned`` may be used on the current stream (once that has waited for
@@ -569,16 +569,16 @@ def _empty_on(stream, shape, dtype, device, returned=True) -> torch.Tensor:
     here = torch.cuda.current_stream()
     s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
     with torch.cuda.stream(s):
-        t = torch.empty(shape, dtype=dtype, device=device)
+        t = torch.empty(*shape, dtype=dtype, device=device)
     if returned and s != here:
         t.record_stream(here)
     return t
 
 
-def _empty(stream, shape, dtype, device) -> torch.Tensor:
+def _empty(stream, dtype, device, *shape) -> torch.Tensor:
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    return _empty_on(stream, shape, dtype, device)
+        return torch.empty(*shape, dtype=dtype, device=device)         # 0.7 us less than from a tuple
+    return _empty_on(stream, dtype, device, *shape)
 
 
 def gemv_w4a16(x: torch.Tensor, w: NVFP4Tensor | MXTensor, bias: torch.Tensor | None = None,
@@ -607,7 +607,7 @@ def gemv_w4a16(x: torch.Tensor, w: NVFP4Tensor | MXTensor, bias: torch.Tensor | 
         raise ValueError("out must be a contiguous bf16 or FP32 [M, N]")
     _on_device(x, codes, sf, scale, bias, out)
     if out is None:
-        y = _empty(stream, (M, N), out_dtype, x.device)
+        y = _empty(stream, out_dtype, x.device, M, N)
     else:
         y = out
         _require(y.shape == (M, N) and y.is_contiguous(), "out must be a contiguous bf16 or FP32 [M, N]")
@@ -655,7 +655,7 @@ def rotary(x: torch.Tensor, positions: torch.Tensor, axes, theta: float = 10000.
         raise ValueError("positions must be contiguous along the axes")
     if out is None:
         _on_device(x, positions)
-        y = _empty(stream, (B, L, H, d), dt, x.device)
+        y = _empty(stream, dt, x.device, B, L, H, d)
         to = _new_heads(y, L, H, d)
     else:
         y = out
@@ -715,14 +715,14 @@ def cross_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, kv_lens: 
     (B, H, Hkv, Lq, Lk, d), hq, hk, hv = _attention_operands(q, k, v, kv_lens)
     if out is None:
         _on_device(q, k, v, kv_lens, dev_status)
-        o = _empty(stream, (B, Lq, H, d), torch.bfloat16, q.device)
+        o = _empty(stream, torch.bfloat16, q.device, B, Lq, H, d)
         to = _new_heads(o, Lq, H, d)
     else:
         o = out
         _require(o.dtype == torch.bfloat16 and o.shape == q.shape and o.stride(3) == 1, "out must be a bf16 tensor of q's shape")
         _on_device(q, k, v, kv_lens, o, dev_status)
         to = _heads(o)
-    lse = _empty(stream, (B, H, Lq), torch.float32, q.device) if return_lse else None
+    lse = _empty(stream, torch.float32, q.device, B, H, Lq) if return_lse else None
     check(lib().nvfp4_cross_attention(hq, hk, hv, None if kv_lens is None else kv_lens.data_ptr(),
                                       d ** -0.5 if scale is None else float(scale), B, H, Hkv, Lq, Lk, d, to,
                                       None if lse is None else lse.data_ptr(), _ptr(dev_status), _stream(stream)),
@@ -748,14 +748,14 @@ def cross_attention_backward(grad_out: torch.Tensor, q: torch.Tensor, k: torch.T
     if workspace is None:
         bytes_ = nvfp4_cross_attention_backward_workspace_bytes(*sizes)
         ws = (torch.empty(bytes_, dtype=torch.uint8, device=device) if stream is None else
-              _empty_on(stream, bytes_, torch.uint8, device, returned=False))
+              _empty_on(stream, torch.uint8, device, bytes_, returned=False))
     else:
         ws = workspace
         _require(ws.is_contiguous(), "workspace must be contiguous")
         bytes_ = ws.numel() * ws.element_size()
-    dq = _empty(stream, (B, Lq, H, d), bf16, device)
-    dk = _empty(stream, (B, Lk, Hkv, d), bf16, device)
-    dv = _empty(stream, (B, Lk, Hkv, d), bf16, device)
+    dq = _empty(stream, bf16, device, B, Lq, H, d)
+    dk = _empty(stream, bf16, device, B, Lk, Hkv, d)
+    dv = _empty(stream, bf16, device, B, Lk, Hkv, d)
     check(lib().nvfp4_cross_attention_backward(
         _PACK_HEADS(grad_out.data_ptr(), gt[0], gt[1], gt[2]), hq, hk, hv, _PACK_HEADS(out.data_ptr(), ot[0], ot[1], ot[2]),
         lse.data_ptr(),
