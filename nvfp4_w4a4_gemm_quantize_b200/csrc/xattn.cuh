@@ -224,13 +224,14 @@ __device__ __forceinline__ F2 mul2(F2 a, F2 b) {
 
 // 2^x of two values on the FMA pipes, for -inf <= x < 127: x = n + r with |r| <=
 // 1/2, 2^r by the polynomial of degree 5 of least relative error (Remez exchange,
-// 2^-23.7; 2^-22.1 with the roundings of FP32), times 2^n.  Below -126, at
-// -infinity too, it is 2^-126 (a sum of nothing else has to be told apart by its
-// maximum); NaN stays NaN.  The hardware exponential does 16 values a cycle and SM,
-// and a tile of 128 x 128 takes 1024 cycles of it: a part goes this way.
+// 2^-23.7; 2^-22.1 with the roundings of FP32), times 2^n.  x is taken as at least
+// -127, where the factor's exponent field is 0: zero from -126.5 down, at -infinity
+// too, as the hardware exponential gives it below -126; NaN stays NaN.  The hardware
+// exponential does 16 values a cycle and SM, and a tile of 128 x 128 takes 1024
+// cycles of it: a part goes this way.
 __device__ __forceinline__ F2 ex2_fma(F2 x) {
-    asm("max.NaN.f32 %0, %0, 0fC2FC0000;" : "+f"(x.x));
-    asm("max.NaN.f32 %0, %0, 0fC2FC0000;" : "+f"(x.y));
+    asm("max.NaN.f32 %0, %0, 0fC2FE0000;" : "+f"(x.x));
+    asm("max.NaN.f32 %0, %0, 0fC2FE0000;" : "+f"(x.y));
     const F2 m = {12583039.0f, 12583039.0f};                // 1.5 * 2^23 + 127: n + 127 in the low bits
     const F2 t = add2(x, m);
     const F2 u = add2(t, {-m.x, -m.y});

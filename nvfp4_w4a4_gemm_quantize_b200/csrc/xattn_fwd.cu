@@ -377,8 +377,7 @@ xattn_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
                 const bool move = mt > m + 8.0f;
                 const float mref = move ? mt : m;
                 const float alpha = move ? ex2(m - mt) : 1.0f;     // m = -infinity: 0
-                // all logits -infinity so far: P is next to nothing (0, or 2^-126 where ex2_fma forms it), not NaN, for a
-                // later key may rule the row; a row that ends so is set to NaN below
+                // all logits -infinity so far: P is 0, not NaN
                 const float mm = mref == -INFINITY ? 0.0f : -mref;
                 F2 sum[2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};
 #pragma unroll
@@ -428,8 +427,7 @@ xattn_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
                     for (int i = 0; i < p.d; i += 8) *reinterpret_cast<uint4*>(orow + i) = make_uint4(0, 0, 0, 0);
                 continue;
             }
-            // no logit above -infinity: 0 / 0 (l holds what ex2_fma left of each of its pairs)
-            inv = m == -INFINITY ? __uint_as_float(0x7FC00000u) : __frcp_rn(l);
+            inv = __frcp_rn(l);                     // no logit above -infinity: 0 / 0
             out_b = item.b;
             out_head = head;
             out_q0 = q0;

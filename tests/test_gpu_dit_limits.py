@@ -228,3 +228,28 @@ def test_training_step_with_a_status(cuda_ok):
     assert torch.equal(out, plain) and all(torch.equal(a, b) for a, b in zip(*grads)) and int(status.item()) == 0
     with pytest.raises(ValueError):
         nv.CrossAttention.apply(q, k, v, None, None, status.cpu())
+
+
+@pytest.mark.parametrize("Lq", [4, 200])
+@pytest.mark.parametrize("low", [-float("inf"), -300.0])
+def test_keys_that_weigh_nothing_beside_huge_values(cuda_ok, Lq, low):
+    """Keys at logits of -infinity, or 200 and more below the row's others, have
+    P below 2^-250: their values of 3e38 add less than 1e-36, and a gradient of
+    3e38 leaves less than 1e-36 in theirs.  (A P that stops at 2^-126 would add
+    3.5.)"""
+    g = torch.Generator(device="cuda").manual_seed(Lq)
+    q, k, v, do = (torch.randn(1, n, 2, 64, generator=g, device="cuda").bfloat16() for n in (Lq, 300, 300, Lq))
+    q[..., 0] = 8.0
+    k[..., 0] = 0.0
+    gone = torch.arange(300, device="cuda") % 3 != 0
+    base, base_lse = nv.cross_attention(q, k[:, ~gone].contiguous(), v[:, ~gone].contiguous(), return_lse=True)
+    k[:, gone, :, 0] = low                                   # logits: 8 low / 8, the rest at most 30 or so
+    v[:, gone] = 3e38
+    out, lse = nv.cross_attention(q, k, v, return_lse=True)
+    # the same sums in another order and other tiles: both within (h + h + 2^-16) of sum P |v| <= max |v|
+    bound = 2.0 * (2 * 2.0 ** -8 + 2.0 ** -16) * float(v[:, ~gone].float().abs().max())
+    assert float((out.float() - base.float()).abs().max()) <= bound
+    assert float((lse - base_lse).abs().max()) <= 2.0 ** -16 * float(base_lse.abs().max() + 1)
+    do[:, 0] = 3e38
+    dv = nv.cross_attention_backward(do, q, k, v, out, lse)[2]
+    assert float(dv[:, gone].float().abs().max()) <= 1e-36
