@@ -40,9 +40,6 @@ namespace xattn {
 constexpr int kBwdThreads = 640;
 constexpr int kBwdWarps = 16;                 // on a tile
 constexpr int kBwdCols = 32;                  // columns of one
-// Of eight pairs of exponentials, on the FMA pipes.  dQ and dK/dV of two clips (8192 x 512, 24 heads of 128) with 0, 2,
-// 4, 6: 170 + 203, 170 + 202, 159 + 175, 165 + 187 us.
-constexpr int kPolyPairs = 4;
 constexpr int kBwdRegsLow = 64;               // 128 x 64 + 512 x 104 <= 640 x 96
 constexpr int kBwdRegsHigh = 104;
 static_assert(128 * kBwdRegsLow + 512 * kBwdRegsHigh <= kBwdThreads * 96, "register split exceeds the launch budget");
@@ -473,10 +470,9 @@ xattn_dq_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
                 }
 #pragma unroll
                 for (int i = 0; i < 32; i += 2) {
-                    const F2 x = ex2_pair<kPolyPairs>(
-                        fma2({__uint_as_float(v[i]), __uint_as_float(v[i + 1])}, {p.c, p.c}, {-lse2, -lse2}), i / 2);
-                    v[i] = __float_as_uint(x.x);
-                    v[i + 1] = __float_as_uint(x.y);
+                    const F2 x = fma2({__uint_as_float(v[i]), __uint_as_float(v[i + 1])}, {p.c, p.c}, {-lse2, -lse2});
+                    v[i] = __float_as_uint(ex2(x.x));
+                    v[i + 1] = __float_as_uint(ex2(x.y));
                 }
                 if (pending) {
                     if (!(ok = read_out(prev))) break;
@@ -756,14 +752,12 @@ xattn_dkv_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const float4 l = lse4[i];                            // kept negated
-                const F2 x = ex2_pair<kPolyPairs>(
-                    fma2({__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1])}, {p.c, p.c}, {l.x, l.y}), 2 * i);
-                const F2 y = ex2_pair<kPolyPairs>(
-                    fma2({__uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3])}, {p.c, p.c}, {l.z, l.w}), 2 * i + 1);
-                v[4 * i] = __float_as_uint(x.x);
-                v[4 * i + 1] = __float_as_uint(x.y);
-                v[4 * i + 2] = __float_as_uint(y.x);
-                v[4 * i + 3] = __float_as_uint(y.y);
+                const F2 x = fma2({__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1])}, {p.c, p.c}, {l.x, l.y});
+                const F2 y = fma2({__uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3])}, {p.c, p.c}, {l.z, l.w});
+                v[4 * i] = __float_as_uint(ex2(x.x));
+                v[4 * i + 1] = __float_as_uint(ex2(x.y));
+                v[4 * i + 2] = __float_as_uint(ex2(y.x));
+                v[4 * i + 3] = __float_as_uint(ex2(y.y));
                 w[2 * i] = pack_bf16(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]));
                 w[2 * i + 1] = pack_bf16(__uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3]));
             }
