@@ -228,7 +228,7 @@ __device__ __forceinline__ F2 mul2(F2 a, F2 b) {
 // -127, where the factor's exponent field is 0: zero from -126.5 down, at -infinity
 // too, as the hardware exponential gives it below -126; NaN stays NaN.  The hardware
 // exponential does 16 values a cycle and SM, and a tile of 128 x 128 takes 1024
-// cycles of it: a part goes this way.
+// cycles of it: where those hold up a kernel, a part goes this way.
 __device__ __forceinline__ F2 ex2_fma(F2 x) {
     asm("max.NaN.f32 %0, %0, 0fC2FE0000;" : "+f"(x.x));
     asm("max.NaN.f32 %0, %0, 0fC2FE0000;" : "+f"(x.y));

@@ -24,12 +24,19 @@
 // registers, a row per thread, it took 6400 cycles an item (a 128-byte line per
 // lane and store), as long as two steps.  It is read out once the next item's
 // first P is stored, so that the wait for the last product has gone by.
-// Bound by a tile's chain, softmax -> P V -> next S -> softmax, 3800 cycles a pair
-// of tiles: the exponentials take 2048 of a pair and its products at d = 128 as
-// much, but the two tiles' exponentials overlap in part, each hand-over between
-// warps and tensor core takes 200 to 300, and the issuing warp, next to busy ones,
-// needs about as long for a product as the tensor core.
-// B200, 32768 queries x 512 states, 24 heads of 128: 209 us (986 TFLOP/s).
+// P is rounded to bf16 for P V, as the tensor core wants both operands in one type
+// and V is bf16: the output is 2.2e-3 off the formula in 64 bits (relative, in the
+// norm) where FP32 arithmetic rounded once is 1.7e-3; P as TF32 would halve the rate.
+// Bound by a tile's chain, softmax -> P V -> next S -> softmax: a tile has one S,
+// and P takes its place.  A step (128 keys of a pair of tiles) takes 3400 to 3600
+// cycles, for heads of 72 as for 128 (the slope over 512 to 2048 keys): its
+// exponentials take 2048 of the hardware's unit and its products at d = 128 as much
+// of the tensor core, but those of the two tiles overlap in part, each hand-over
+// between warps and tensor core takes 200 to 300, and the issuing warp, next to busy
+// ones, needs about as long for a product as the tensor core.  An item's start and
+// end come to 5000 to 7000 on top: 4900 a step for items of four.
+// B200, 32768 queries x 512 states, 24 heads of 128: 214 us (963 TFLOP/s) in a burst
+// at 1965 MHz, 220 to 235 sustained, where the 1000 W limit holds 1.73 GHz.
 #include "xattn.cuh"
 
 namespace nvfp4 {
@@ -39,9 +46,6 @@ constexpr int kThreads = 384;
 constexpr int kQBufs = 4;                     // two items' tiles: an output leaves from its own during the next item's steps
 static_assert(kQBufs >= 4, "an item would wait for the tiles of the one before it, and that one for this item");
 constexpr int kMaxRing = 12;
-// Of eight pairs of exponentials, on the FMA pipes.  32768 queries x 512 states, 24 heads of 128, with 0 to 3: 242, 235,
-// 247, 266 us (two softmax warps per scheduler: more is bound by their instructions).
-constexpr int kPolyPairs = 1;
 constexpr int kRegsLow = 88;                  // 128 x 88 + 256 x 208 <= 384 x 168
 constexpr int kRegsHigh = 208;
 static_assert(128 * kRegsLow + 256 * kRegsHigh <= kThreads * 168, "register split exceeds the launch budget");
@@ -386,8 +390,10 @@ xattn_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
                     uint32_t w[16];
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
-                        const F2 e = ex2_pair<kPolyPairs>(fma2({__uint_as_float(v[c2 * 32 + 2 * i]), __uint_as_float(v[c2 * 32 + 2 * i + 1])},
-                                                               {p.c, p.c}, {mm, mm}), i);
+                        // (all on the hardware's unit: 32768 queries x 512 states, 24 heads of 128, take 214, 214, 231, 246 us
+                        // with 0 to 3 of eight pairs on the FMA pipes, two softmax warps per scheduler being bound by instructions)
+                        const F2 x = fma2({__uint_as_float(v[c2 * 32 + 2 * i]), __uint_as_float(v[c2 * 32 + 2 * i + 1])}, {p.c, p.c}, {mm, mm});
+                        const F2 e = {ex2(x.x), ex2(x.y)};
                         sum[i & 1] = add2(sum[i & 1], e);
                         w[i] = pack_bf16(e.x, e.y);
                     }
