@@ -25,9 +25,11 @@
 // products are of unscaled codes, arranged so that their sums come apart by block,
 // and the scales multiply those in FP32.  A block that finds a wider range, or a
 // value that is not finite, decodes to bf16 instead.
-// B200: 5120 -> 20480, NVFP4, one row 19.2 us (59 MB: 9.0 at the copy rate; the x
-// and the first items take 5, decoding keeps the ALU half busy); 20480 -> 5120, MX,
-// sixteen rows 36.9 us (15 clusters of 8 hold 120 of the 148 SMs; x 10, the join 5).
+// B200: 5120 -> 20480, NVFP4, one row 19.7 us (59 MB: 9.0 at the copy rate): the ALU
+// pipe is 47 % busy, the issue slots 45 %, DRAM 44 %, so nothing bounds it but its
+// start (x and the first items, 5 us, in which nothing is decoded) and the latency of
+// a warp's one item at a time.  20480 -> 5120, MX, sixteen rows 36.9 us (15 clusters
+// of 8 hold 120 of the 148 SMs; x 10, the join 5, issue slots 50 % busy).
 // Items through shared memory, four ahead, against two in registers: 21 and 36 us
 // against 24 and 40.5; 2 x 4 blocks and a 128-feature tile each: 28 and 48.
 #include <atomic>
@@ -724,8 +726,12 @@ cudaError_t launch_gemv(const GemvArgs& a, int num_sms, cudaStream_t stream) {
     p.units = (a.N + 127) / 128 * 4;
     p.steps = (a.K + kStepK - 1) / kStepK;
     p.kb4 = a.K / (a.mx ? 128 : 64);
-    // Blocks along k: the number that ends first, in items of a warp; a cluster's start and join cost about two, a block
-    // reads its part of x first.  The clusters all run at once: more of them than the GPCs hold would double the time.
+    // Blocks along k: the number that ends first, in sixteenths of a round of items (one item of each warp); a cluster's
+    // start and join cost about two rounds, and a block reads, scans and converts its part of x first, 128 k of a row
+    // for a 9th of a sixteenth.  (Against each number by force, 6 shapes of both formats at 1, 4, 8 and 16 rows: the
+    // choice is within 5 % of the best in 30 of these 48 and up to 1.5 times it in the rest, 4 rows of 5120 -> 5120
+    // 18.5 us for 12.3.  There x costs more than the 9th: 0.03 us a row and 128 k, where a round takes 1.2 us at one row
+    // and 2.4 at sixteen.)  The clusters all run at once: more of them than the GPCs hold would double the time.
     int ranks = 1, clusters = 1;
     int64_t best = 0;
     for (int r = 1; r <= kMaxCluster && r <= p.steps; r *= 2) {

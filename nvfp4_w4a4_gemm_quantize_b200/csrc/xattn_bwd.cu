@@ -9,13 +9,21 @@
 // computed in both of the latter, seven tile products in place of five: the sums
 // of either stay in tensor memory, so nothing is added in global memory and the
 // order of every sum is fixed.
-// B200, 2 x 8192 queries x (512, 389) states, 24 heads of 128: D 35 us (its bytes
-// 31), dQ 159, dK and dV 175, their join 20.  A step of dQ takes 2850 cycles, 1536
-// of them the tensor core's, one of dK and dV 3300, 2048 of them (58 % busy): the
-// one issuing warp shares its scheduler with busy warps, and its waits on barriers
-// that are complete take 170 to 290 cycles each.  (Two issuing warps, one a pair of
-// products, were slower, 217 us for dK and dV: their products alternate on the
-// tensor core.)
+// P and dS are rounded to bf16 for their products, as K, Q and dO are bf16 and the
+// tensor core wants both operands in one type: the gradients are 2.4e-3 off the
+// formula in 64 bits (relative, in the norm) where FP32 arithmetic rounded once is
+// 1.7e-3.  D of samples of several key tiles comes from the bf16 O, which it would
+// otherwise take another pass over the keys to replace; its error counts where
+// dP - D is small, with few keys, and those samples form D from P and dP.
+// B200, 2 x 8192 queries x (512, 389) states, 24 heads of 128, each kernel alone: D
+// 36 us (its bytes 31), dQ 167, dK and dV 195, their join 21; the whole 412 in a
+// burst, 438 sustained under the 1000 W limit.  A step takes 2510 to 2580 cycles in
+// dQ, 1536 of them the tensor core's, and 3150 to 3300 in dK and dV, 2048 of them
+// (the slope over 512 to 2048 keys; starts and ends bring the whole launch to 43 and
+// 58 % of the tensor core): the one issuing warp shares its scheduler with busy
+// warps, and its waits on barriers that are complete take 170 to 290 cycles each.
+// (Two issuing warps, one a pair of products, were slower, by a tenth for dK and dV:
+// their products alternate on the tensor core.)
 //
 // dQ (dq_kernel): persistent, a work item is a 128-query tile of one head, its
 // steps are key tiles of 128.  TMEM: two S, one dP = dO V^T, dQ.  dS overwrites
@@ -41,7 +49,7 @@ constexpr int kBwdThreads = 640;
 constexpr int kBwdWarps = 16;                 // on a tile
 constexpr int kBwdCols = 32;                  // columns of one
 // Of eight pairs of dK/dV's exponentials, on the FMA pipes: a step of 128 x 128, d = 128, takes 3150 to 3300 cycles with 4,
-// 3410 with none (they come between two hand-overs).  dQ's run beside its products: 2590 with 4, 2510 to 2560 with none.
+// 3410 with none (they come between two hand-overs).  dQ's run beside its products: 2590 with 4, 2510 to 2580 with none.
 constexpr int kPolyPairs = 4;
 constexpr int kBwdRegsLow = 64;               // 128 x 64 + 512 x 104 <= 640 x 96
 constexpr int kBwdRegsHigh = 104;
@@ -887,6 +895,8 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const float* partial
 // Ranges of the query tiles of a key tile: the number that ends first, counted in steps, where each block costs
 // kSplitCost steps beside its own (start, last sums and their share of the join).
 constexpr int kSplitCost = 3;
+// The SMs of the GPUs that the library runs on.  The plan sizes the workspace, which is asked for by sizes alone, on hosts
+// without a GPU too, and has to be the same wherever the call then runs: it does not ask the device.
 constexpr int kPlanSms = 148;
 
 int split_count(int64_t units, int64_t steps) {

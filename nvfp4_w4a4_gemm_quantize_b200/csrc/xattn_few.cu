@@ -4,7 +4,9 @@
 //
 // Bound by reading K and V once.  The rows are the A operand of m16n8k16 products,
 // S = Q K^T and O += P V, with an online softmax in registers (P goes from the
-// first product's sums to the second's A operand without leaving the lane).
+// first product's sums to the second's A operand without leaving the lane, rounded
+// to bf16 as V is: the output is 2.1e-3 off the formula in 64 bits, in the norm,
+// where FP32 arithmetic rounded once is 1.7e-3).
 // Every warp is a stream of its own over a range of the keys: it loads slices of
 // 32 keys of K and V by TMA into a ring of its own and refills a slot when it has
 // used it, so nothing in the loop waits for another warp.  The keys of a (sample,

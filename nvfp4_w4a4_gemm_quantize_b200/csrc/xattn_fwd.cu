@@ -28,7 +28,7 @@
 // and V is bf16: the output is 2.2e-3 off the formula in 64 bits (relative, in the
 // norm) where FP32 arithmetic rounded once is 1.7e-3; P as TF32 would halve the rate.
 // Bound by a tile's chain, softmax -> P V -> next S -> softmax: a tile has one S,
-// and P takes its place.  A step (128 keys of a pair of tiles) takes 3400 to 3600
+// and P takes its place.  A step (128 keys of a pair of tiles) takes 3550 to 3600
 // cycles, for heads of 72 as for 128 (the slope over 512 to 2048 keys): its
 // exponentials take 2048 of the hardware's unit and its products at d = 128 as much
 // of the tensor core, but those of the two tiles overlap in part, each hand-over
