@@ -36,7 +36,7 @@
 // ones, needs about as long for a product as the tensor core.  An item's start and
 // end come to 5000 to 7000 on top: 4900 a step for items of four.
 // B200, 32768 queries x 512 states, 24 heads of 128: 214 us (963 TFLOP/s) in a burst
-// at 1965 MHz, 220 to 235 sustained, where the 1000 W limit holds 1.73 GHz.
+// at 1965 MHz, 220 to 240 sustained, where the 1000 W limit holds 1.73 GHz.
 #include "xattn.cuh"
 
 namespace nvfp4 {
